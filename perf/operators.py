@@ -308,7 +308,7 @@ def _own_norm(st, case):
 def _own_norm_bwd(st, case):
     moe, s, ws = _handle(st, case)
     moe.moe_rms_norm_backward(s, st["dy"], st["dres"], st.get("h"), st.get("codes"), st.get("scales"), st["rstd"],
-                              st["weight"], st["dx"], st["dweight"], ws)
+                              st["weight"], None, st["dx"], st["dweight"], ws)
     return {"dx": st["dx"], "dweight": st["dweight"]}
 
 
@@ -324,8 +324,8 @@ def _own_balance(st, case):
 def _own_route_bwd(st, case):
     moe, s, ws = _handle(st, case)
     moe.moe_route_backward(s, st.get("x"), st.get("codes"), st.get("scales"), st.get("weight"), st["wr"],
-                           case["renorm"], st["z"], st["ids"], st["topw"], st["dw"], st["dz_in"], st["dx"],
-                           st["dwr"], st["db"], ws)
+                           case["renorm"], st["z"], st["ids"], st["topw"], st["dw"], st["dz_in"], None,
+                           st["dx"], st["dwr"], st["db"], ws)
     return {"dx": st["dx"], "dwr": st["dwr"], "db": st["db"]}
 
 
