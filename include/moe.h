@@ -315,6 +315,123 @@ moe_status moe_residency_swap(const moe_shape *s, const moe_residency *r, const 
 moe_status moe_fingerprint(const moe_shape *s, const moe_residency *r, const int32_t *experts, int32_t n,
                            uint64_t *out, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The norm in front of the layer and the router's training side: the RMS norm
+ * with the residual's addition, the balance loss, and the backward of norm and
+ * router.  (The experts' MXFP4 weights are frozen: they have no gradient
+ * here.)  All of it is deterministic: every sum has an order that depends on
+ * the sizes alone.
+ *
+ * Besides the conventions above:
+ *   - Only s->hidden, n_experts and top_k matter (inter must be valid).
+ *   - Element types are moe_out_dtype values (MOE_OUT_F32, MOE_OUT_BF16).
+ *   - All memory must be of the current device (or mapped host memory), and
+ *     `stream` of that device too, else MOE_ERR_INVALID_ARG.
+ *   - An output may not overlap another argument, except where an entry names
+ *     an argument it may replace in place (same address and type).
+ *   - token_mask (uint8 [T] or NULL): a token whose entry is 0 takes no part in
+ *     any sum, whatever its rows hold (NaN included), and its gradient rows
+ *     are written as zeros.
+ *   - Scratch: `ws` of at least moe_train_workspace_bytes(s, T, n_seq) bytes,
+ *     256-byte aligned, on the rules of the layer's workspace.  Two captured
+ *     graphs that may run at the same time need a workspace each.
+ *   - T = 0 writes the outputs that are sums over tokens (zeros) and nothing
+ *     else.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of workspace for the entries below, for T tokens in n_seq sequences
+ * (0 if an argument is invalid; n_seq in [1, MOE_MAX_SEQS]). */
+#define MOE_MAX_SEQS 32768
+size_t moe_train_workspace_bytes(const moe_shape *s, int32_t n_tokens, int32_t n_seq);
+
+/* The 8-bit output of moe_rms_norm: none, of y, or of the normalised values
+ * before the weight (the checkpoint the backward entries read).
+ * Codes are OCP e4m3 [T][H], scales e8m0 [T][H/32], one per 32 consecutive
+ * elements: scale 2^e with e the least in [-127, 127] for which the block's
+ * largest magnitude is at most 448 2^e; a code is the value over its scale
+ * rounded to the nearest (half to even).  A block with a non-finite value has
+ * scale byte 255 (NaN). */
+typedef enum { MOE_Q_NONE = 0, MOE_Q_OUTPUT = 1, MOE_Q_NORMALIZED = 2 } moe_q_kind;
+
+/* RMS norm with the residual's addition:
+ *   h = x + residual (fp32 sum, rounded to residual_dtype; h = x without a
+ *   residual, rounded only when residual_out is given),
+ *   r = 1 / sqrt(mean of h^2 over H + eps),  y = h r weight.
+ *   x [T][H] of x_dtype; residual, residual_out [T][H] of residual_dtype, each
+ *   may be NULL, residual_out may be residual (or x, with equal types) in
+ *   place; weight fp32 [H]; y [T][H] bf16 or NULL, may be a bf16 x in place;
+ *   q_codes, q_scales by q_kind (ignored for MOE_Q_NONE); rstd fp32 [T] (the
+ *   r above) or NULL.  At least one of y, residual_out, q must be wanted.
+ *   Tensor rows must be 16-byte aligned.  eps >= 0; with eps = 0 a zero row
+ *   gives NaN. */
+moe_status moe_rms_norm(const moe_shape *s, int32_t n_tokens, int32_t x_dtype, const void *x,
+                        int32_t residual_dtype, const void *residual, const float *weight, float eps,
+                        void *residual_out, uint16_t *y, int32_t q_kind, uint8_t *q_codes, uint8_t *q_scales,
+                        float *rstd, void *stream);
+
+/* Backward of moe_rms_norm.  With n = h r and g = dy weight:
+ *   dx = dresidual + r (g - n mean of (g n) over H)   (the gradient of x and of
+ *        the residual alike),  dweight = sum over tokens of dy n.
+ *   dy [T][H] of dy_dtype; dresidual [T][H] of dresidual_dtype or NULL; n from h
+ *   ([T][H] of h_dtype: moe_rms_norm's residual_out, or its x where there was
+ *   neither residual nor residual_out) or, with h NULL, from the
+ *   MOE_Q_NORMALIZED checkpoint q_codes, q_scales; rstd fp32 [T]; dx [T][H] of
+ *   dx_dtype or NULL, may be dy, dresidual or h in place (equal types);
+ *   dweight fp32 [H] or NULL.  Sums are fp32. */
+moe_status moe_rms_norm_backward(const moe_shape *s, int32_t n_tokens, int32_t dy_dtype, const void *dy,
+                                 int32_t dresidual_dtype, const void *dresidual, int32_t h_dtype, const void *h,
+                                 const uint8_t *q_codes, const uint8_t *q_scales, const float *rstd,
+                                 const float *weight, const uint8_t *token_mask, int32_t dx_dtype, void *dx,
+                                 float *dweight, void *ws, size_t ws_bytes, void *stream);
+
+/* Balance loss of the router's softmax over all E, and the picks' counts.
+ * seq_offsets (int32 [n_seq+1], not decreasing, or NULL with n_seq = 1: one
+ * group of all tokens): sequence g holds the tokens [off[g], off[g+1]);
+ * tokens outside every sequence count nowhere.  With N_g the tokens of g that
+ * count, counts[g][e] the picks of e among them (ids outside [0, E) not
+ * counted) and P[g][e] their mean probability (0 where N_g = 0):
+ *   loss = alpha / S' sum over the S' sequences with N_g > 0 of
+ *          sum_e (E counts[g][e] / (k N_g)) P[g][e]        (0 if there is none).
+ *   logits fp32 [T][E]; topk_ids [T][k]; loss fp32 [1]; counts int32
+ *   [n_seq][E]; n_valid int32 [n_seq+1]: N_g, then S'; prob_mean fp32
+ *   [n_seq][E] (P) or NULL.  A logit of -inf has probability 0, also in a row
+ *   of nothing else; NaN or +inf make their sequence's P and the loss NaN. */
+moe_status moe_balance_loss(const moe_shape *s, int32_t n_tokens, const float *logits, const int32_t *topk_ids,
+                            const uint8_t *token_mask, const int32_t *seq_offsets, int32_t n_seq, float alpha,
+                            float *loss, int32_t *counts, int32_t *n_valid, float *prob_mean, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/* Gradient of moe_balance_loss with respect to the logits (the counts, being
+ * piecewise constant, pass none), times *dloss (fp32 [1]; NULL: 1).  counts
+ * and n_valid as the forward wrote them; dlogits fp32 [T][E], may be logits in
+ * place; rows of tokens in no sequence are zeros. */
+moe_status moe_balance_loss_backward(const moe_shape *s, int32_t n_tokens, const float *logits,
+                                     const uint8_t *token_mask, const int32_t *seq_offsets, int32_t n_seq,
+                                     float alpha, const float *dloss, const int32_t *counts, const int32_t *n_valid,
+                                     float *dlogits, void *stream);
+
+/* Backward of moe_route.  dz = the gradient of topk_w carried to the logits
+ * (renormalize as in the forward) plus dlogits_in, then dx = dz w_router,
+ * dw_router = dz^T x, dbias = sum over tokens of dz.
+ *   x [T][H] bf16, or NULL with the layer's input as a checkpoint of
+ *   moe_rms_norm: q_codes, q_scales, and q_weight = the norm's weight (fp32
+ *   [H]) for MOE_Q_NORMALIZED or NULL for MOE_Q_OUTPUT (none of the three is
+ *   read when dw_router is NULL); w_router fp32 [E][H] (read for dx); logits
+ *   fp32 [T][E] (read when renormalize == 0 and dtopk_w is given); topk_ids,
+ *   topk_w as the forward wrote them and dtopk_w fp32 [T][k] (NULL: no
+ *   gradient from the weights; then topk_ids and topk_w are not read); an id
+ *   outside [0, E) has no gradient; dlogits_in fp32 [T][E] or NULL; dx [T][H]
+ *   of dx_dtype, dw_router fp32 [E][H], dbias fp32 [E], each NULL if not
+ *   wanted.  At least one of dtopk_w and dlogits_in, and one output, must be
+ *   given.  A non-finite factor makes the sums it enters non-finite (infinite
+ *   or NaN). */
+moe_status moe_route_backward(const moe_shape *s, int32_t n_tokens, const uint16_t *x, const uint8_t *q_codes,
+                              const uint8_t *q_scales, const float *q_weight, const float *w_router,
+                              int32_t renormalize, const float *logits, const int32_t *topk_ids,
+                              const float *topk_w, const float *dtopk_w, const float *dlogits_in,
+                              const uint8_t *token_mask, int32_t dx_dtype, void *dx, float *dw_router,
+                              float *dbias, void *ws, size_t ws_bytes, void *stream);
+
 /* Per-kernel timing, a tracing aid (off by default).  While enabled, each
  * kernel the library enqueues carries a start/stop HIP event pair stamped by
  * its own dispatch, so the times are kernel execution times.

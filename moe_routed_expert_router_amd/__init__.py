@@ -15,4 +15,6 @@ from ._lib import (  # noqa: F401
     MOE_MAX_SWAPS, moe_count_picks, moe_residency_plan, moe_residency_swap, moe_fingerprint,
     moe_profile_enable, moe_profile_reset, moe_profile_read, moe_probe_read, moe_probe_mfma,
     MOE_NOALLOC_WS_BYTES, moe_layer_forward_noalloc,
+    MOE_Q_NONE, MOE_Q_OUTPUT, MOE_Q_NORMALIZED, MOE_MAX_SEQS, moe_train_workspace_bytes, moe_rms_norm,
+    moe_rms_norm_backward, moe_balance_loss, moe_balance_loss_backward, moe_route_backward,
 )

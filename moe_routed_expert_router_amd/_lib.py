@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_int32, c_size_t, c_void_p, c_char_p, POINTER
+from ctypes import c_float, c_int32, c_size_t, c_void_p, c_char_p, POINTER
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
@@ -22,6 +22,8 @@ EXPORTS = (
     "moe_count_picks", "moe_residency_plan", "moe_residency_swap", "moe_fingerprint",
     "moe_profile_enable", "moe_profile_reset", "moe_profile_read", "moe_probe_read", "moe_probe_mfma",
     "moe_layer_forward_noalloc",
+    "moe_train_workspace_bytes", "moe_rms_norm", "moe_rms_norm_backward", "moe_balance_loss",
+    "moe_balance_loss_backward", "moe_route_backward",
 )
 
 MOE_OK = 0
@@ -33,6 +35,8 @@ MOE_ERR_BAD_RESIDENCY = 5
 MOE_ERR_WORKSPACE_TOO_SMALL = 6
 MOE_ERR_HIP = 7
 MOE_OUT_F32, MOE_OUT_BF16 = 0, 1
+MOE_Q_NONE, MOE_Q_OUTPUT, MOE_Q_NORMALIZED = 0, 1, 2
+MOE_MAX_SEQS = 32768
 
 
 class MoeError(RuntimeError):
@@ -92,6 +96,17 @@ def _load():
         "moe_probe_mfma": (c_int32, [c_int32, c_int32, P, P]),
         "moe_layer_forward_noalloc": (c_int32, [POINTER(MoeShape), c_int32, P, P, P, c_int32,
                                                 POINTER(MoeResidency), P, P, c_int32, P, P]),
+        "moe_train_workspace_bytes": (c_size_t, [POINTER(MoeShape), c_int32, c_int32]),
+        "moe_rms_norm": (c_int32, [POINTER(MoeShape), c_int32, c_int32, P, c_int32, P, P, c_float, P, P, c_int32,
+                                   P, P, P, P]),
+        "moe_rms_norm_backward": (c_int32, [POINTER(MoeShape), c_int32, c_int32, P, c_int32, P, c_int32, P, P, P, P,
+                                            P, P, c_int32, P, P, P, c_size_t, P]),
+        "moe_balance_loss": (c_int32, [POINTER(MoeShape), c_int32, P, P, P, P, c_int32, c_float, P, P, P, P, P,
+                                       c_size_t, P]),
+        "moe_balance_loss_backward": (c_int32, [POINTER(MoeShape), c_int32, P, P, P, c_int32, c_float, P, P, P, P,
+                                                P]),
+        "moe_route_backward": (c_int32, [POINTER(MoeShape), c_int32, P, P, P, P, P, c_int32, P, P, P, P, P, P,
+                                         c_int32, P, P, P, P, c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -266,6 +281,134 @@ def moe_residency_swap(s: MoeShape, r: MoeResidency, pairs, stream=None) -> None
 def moe_fingerprint(s: MoeShape, r: MoeResidency, experts, out, stream=None) -> None:
     _check(lib.moe_fingerprint(ctypes.byref(s), ctypes.byref(r), _ptr(experts), experts.numel(), _ptr(out),
                                _stream(stream)))
+
+
+# ------------------ the norm and the router's training side ------------------
+# Tensors are checked here for type, shape and contiguity (the C entries see
+# addresses only); None stands for NULL.
+def _codes_types():
+    """Types of 8-bit codes and of their scales: bytes, or torch's own types of the same bits."""
+    import torch
+    return (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _fit(name: str, t, shape: tuple, *dtypes):
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _kind(t) -> int:
+    """moe_out_dtype of a tensor that _fit accepted (None: unused)."""
+    import torch
+    return MOE_OUT_F32 if t is not None and t.dtype == torch.float32 else MOE_OUT_BF16
+
+
+def _ws(ws) -> tuple:
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def moe_train_workspace_bytes(s: MoeShape, n_tokens: int, n_seq: int = 1) -> int:
+    return lib.moe_train_workspace_bytes(ctypes.byref(s), n_tokens, n_seq)
+
+
+def moe_rms_norm(s: MoeShape, x, residual, weight, eps: float, residual_out, y, q_kind: int = MOE_Q_NONE,
+                 q_codes=None, q_scales=None, rstd=None, stream=None) -> None:
+    """h = x + residual -> residual_out; y = h r weight (bf16); the 8-bit
+    output by q_kind; rstd = r.  x and the residual are float32 or bfloat16."""
+    import torch
+    T, H = x.shape[0], s.hidden
+    f32, b16 = torch.float32, torch.bfloat16
+    ct, st = _codes_types()
+    p = (_fit("x", x, (T, H), f32, b16), _fit("residual", residual, (T, H), f32, b16),
+         _fit("weight", weight, (H,), f32), _fit("residual_out", residual_out, (T, H), f32, b16),
+         _fit("y", y, (T, H), b16), _fit("q_codes", q_codes, (T, H), *ct),
+         _fit("q_scales", q_scales, (T, H // 32), *st), _fit("rstd", rstd, (T,), f32))
+    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
+        raise TypeError(f"residual is {residual.dtype} and residual_out {residual_out.dtype}: they must agree")
+    _check(lib.moe_rms_norm(ctypes.byref(s), T, _kind(x), p[0], _kind(residual if residual_out is None else residual_out),
+                            p[1], p[2], eps, p[3], p[4], q_kind, p[5], p[6], p[7], _stream(stream)))
+
+
+def moe_rms_norm_backward(s: MoeShape, dy, dresidual, h, q_codes, q_scales, rstd, weight, token_mask, dx, dweight, ws,
+                          stream=None) -> None:
+    """dx and dweight from h, or (h None) from the MOE_Q_NORMALIZED checkpoint."""
+    import torch
+    T, H = dy.shape[0], s.hidden
+    f32, b16 = torch.float32, torch.bfloat16
+    ct, st = _codes_types()
+    p = (_fit("dy", dy, (T, H), f32, b16), _fit("dresidual", dresidual, (T, H), f32, b16),
+         _fit("h", h, (T, H), f32, b16), _fit("q_codes", q_codes, (T, H), *ct),
+         _fit("q_scales", q_scales, (T, H // 32), *st), _fit("rstd", rstd, (T,), f32),
+         _fit("weight", weight, (H,), f32), _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool),
+         _fit("dx", dx, (T, H), f32, b16), _fit("dweight", dweight, (H,), f32))
+    _check(lib.moe_rms_norm_backward(ctypes.byref(s), T, _kind(dy), p[0], _kind(dresidual), p[1], _kind(h), p[2],
+                                     p[3], p[4], p[5], p[6], p[7], _kind(dx), p[8], p[9], *_ws(ws),
+                                     _stream(stream)))
+
+
+def _n_seq(seq_offsets) -> int:
+    return 1 if seq_offsets is None else seq_offsets.numel() - 1
+
+
+def moe_balance_loss(s: MoeShape, logits, topk_ids, token_mask, seq_offsets, alpha: float, loss, counts, n_valid,
+                     prob_mean, ws, stream=None) -> None:
+    """loss, counts [S][E], n_valid [S+1] and prob_mean [S][E] of S sequences
+    (seq_offsets int32 [S+1]; None: one group of all tokens)."""
+    import torch
+    T, E, S = logits.shape[0], s.n_experts, _n_seq(seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    p = (_fit("logits", logits, (T, E), f32), _fit("topk_ids", topk_ids, (T, s.top_k), i32),
+         _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool),
+         _fit("seq_offsets", seq_offsets, (S + 1,), i32), _fit("loss", loss, (1,), f32),
+         _fit("counts", counts, (S, E), i32), _fit("n_valid", n_valid, (S + 1,), i32),
+         _fit("prob_mean", prob_mean, (S, E), f32))
+    _check(lib.moe_balance_loss(ctypes.byref(s), T, p[0], p[1], p[2], p[3], S, alpha, p[4], p[5], p[6], p[7],
+                                *_ws(ws), _stream(stream)))
+
+
+def moe_balance_loss_backward(s: MoeShape, logits, token_mask, seq_offsets, alpha: float, dloss, counts, n_valid,
+                              dlogits, stream=None) -> None:
+    import torch
+    T, E, S = logits.shape[0], s.n_experts, _n_seq(seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    p = (_fit("logits", logits, (T, E), f32), _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool),
+         _fit("seq_offsets", seq_offsets, (S + 1,), i32), _fit("dloss", dloss, (1,), f32),
+         _fit("counts", counts, (S, E), i32), _fit("n_valid", n_valid, (S + 1,), i32),
+         _fit("dlogits", dlogits, (T, E), f32))
+    _check(lib.moe_balance_loss_backward(ctypes.byref(s), T, p[0], p[1], p[2], S, alpha, p[3], p[4], p[5], p[6],
+                                         _stream(stream)))
+
+
+def moe_route_backward(s: MoeShape, x, q_codes, q_scales, q_weight, w_router, renormalize: bool, logits, topk_ids,
+                       topk_w, dtopk_w, dlogits_in, token_mask, dx, dw_router, dbias, ws, stream=None) -> None:
+    """dx, dw_router and dbias (each None if not wanted) from the gradient of
+    the routing weights and / or dlogits_in; the layer's input as x (bfloat16)
+    or as a checkpoint of moe_rms_norm."""
+    import torch
+    H, E, k = s.hidden, s.n_experts, s.top_k
+    g = dtopk_w if dtopk_w is not None else dlogits_in
+    if g is None:
+        raise ValueError("dtopk_w or dlogits_in must be given")
+    T = g.shape[0]
+    f32, b16, i32 = torch.float32, torch.bfloat16, torch.int32
+    ct, st = _codes_types()
+    p = (_fit("x", x, (T, H), b16, torch.int16, torch.uint16), _fit("q_codes", q_codes, (T, H), *ct),
+         _fit("q_scales", q_scales, (T, H // 32), *st), _fit("q_weight", q_weight, (H,), f32),
+         _fit("w_router", w_router, (E, H), f32), _fit("logits", logits, (T, E), f32),
+         _fit("topk_ids", topk_ids, (T, k), i32), _fit("topk_w", topk_w, (T, k), f32),
+         _fit("dtopk_w", dtopk_w, (T, k), f32), _fit("dlogits_in", dlogits_in, (T, E), f32),
+         _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool), _fit("dx", dx, (T, H), f32, b16),
+         _fit("dw_router", dw_router, (E, H), f32), _fit("dbias", dbias, (E,), f32))
+    _check(lib.moe_route_backward(ctypes.byref(s), T, p[0], p[1], p[2], p[3], p[4], int(bool(renormalize)), p[5],
+                                  p[6], p[7], p[8], p[9], p[10], _kind(dx), p[11], p[12], p[13], *_ws(ws),
+                                  _stream(stream)))
 
 
 def moe_profile_enable(on: bool) -> None:

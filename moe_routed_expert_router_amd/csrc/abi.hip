@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "kernels.hpp"
+#include "train/train.hpp"
 
 namespace {
 
@@ -237,6 +238,103 @@ moe_status check_out(const moe_shape *s, int32_t T, int32_t out_dtype, void *out
     if (out_dtype != MOE_OUT_F32 && out_dtype != MOE_OUT_BF16)
         return fail(MOE_ERR_INVALID_ARG, "out_dtype %d unknown", out_dtype);
     return check_ptr(out, (size_t)T * s->hidden * (out_dtype == MOE_OUT_F32 ? 4 : 2), 16, "out");
+}
+
+// Arguments of a training-side call: what each pointer must satisfy, and no
+// output over another argument.  Memory must be of the current device (host
+// memory mapped for the device is as good).
+class ArgCheck {
+public:
+    ArgCheck() {
+        if (hipGetDevice(&dev_) != hipSuccess) {
+            (void)hipGetLastError();
+            dev_ = -1;
+        }
+    }
+    void in(const void *p, size_t bytes, size_t align, const char *name) { add(p, bytes, align, name, false); }
+    void out(const void *p, size_t bytes, size_t align, const char *name) { add(p, bytes, align, name, true); }
+    // `out` may replace `in` in place (checked by the caller: same type)
+    void in_place(const void *out, const void *in) {
+        if (n_pairs_ < kMaxPairs) pairs_[n_pairs_++] = {out, in};
+    }
+    moe_status status(void *stream) {
+        if (st_ != MOE_OK) return st_;
+        for (int i = 0; i < n_; ++i)
+            for (int j = 0; j < n_; ++j)
+                if (b_[i].out && i != j && (j > i || !b_[j].out) && overlap(b_[i], b_[j]) && !allowed(b_[i].p, b_[j].p))
+                    return fail(MOE_ERR_INVALID_ARG, "%s and %s overlap", b_[i].name, b_[j].name);
+        if (stream) {
+            hipDevice_t d = -1;
+            const hipError_t e = hipStreamGetDevice(static_cast<hipStream_t>(stream), &d);
+            if (e != hipSuccess) {
+                (void)hipGetLastError();
+                return fail(MOE_ERR_INVALID_ARG, "stream: %s", hipGetErrorString(e));
+            }
+            if (d != dev_) return fail(MOE_ERR_INVALID_ARG, "stream is of device %d, the current one is %d", d, dev_);
+        }
+        return MOE_OK;
+    }
+
+private:
+    struct Buf {
+        const void *p;
+        size_t bytes;
+        bool out;
+        const char *name;
+    };
+    static constexpr int kMax = 20, kMaxPairs = 4;
+    static bool overlap(const Buf &a, const Buf &b) {
+        const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+        return x < y + b.bytes && y < x + a.bytes;
+    }
+    bool allowed(const void *p, const void *q) const {
+        if (p != q) return false;
+        for (int i = 0; i < n_pairs_; ++i)
+            if (pairs_[i].out == p && pairs_[i].in == q) return true;
+        return false;
+    }
+    void add(const void *p, size_t bytes, size_t align, const char *name, bool out) {
+        if (st_ != MOE_OK) return;
+        if ((st_ = check_ptr(p, bytes, align, name)) != MOE_OK) return;
+        if (dev_ < 0) {
+            st_ = fail(MOE_ERR_HIP, "no usable current device");
+            return;
+        }
+        hipPointerAttribute_t at;
+        if (hipPointerGetAttributes(&at, p) != hipSuccess) {
+            (void)hipGetLastError();
+            st_ = fail(MOE_ERR_NOT_DEVICE_ACCESSIBLE, "%s (%p) is not memory known to HIP", name, p);
+        } else if (at.type == hipMemoryTypeDevice && at.device != dev_) {
+            st_ = fail(MOE_ERR_INVALID_ARG, "%s is memory of device %d, the current one is %d", name, at.device, dev_);
+        } else {
+            b_[n_++] = {p, bytes, out, name};
+        }
+    }
+    int dev_ = -1, n_ = 0, n_pairs_ = 0;
+    moe_status st_ = MOE_OK;
+    Buf b_[kMax];
+    struct Pair {
+        const void *out, *in;
+    } pairs_[kMaxPairs];
+};
+
+moe_status check_dtype(int32_t d, const char *name) {
+    if (d != MOE_OUT_F32 && d != MOE_OUT_BF16) return fail(MOE_ERR_INVALID_ARG, "%s %d unknown", name, d);
+    return MOE_OK;
+}
+
+size_t elem_bytes(int32_t dtype) { return dtype == MOE_OUT_F32 ? 4 : 2; }
+
+moe_status check_seqs(int32_t n_seq) {
+    if (n_seq < 1 || n_seq > MOE_MAX_SEQS)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_seq=%d outside [1, %d]", n_seq, MOE_MAX_SEQS);
+    return MOE_OK;
+}
+
+moe_status check_train_ws(size_t need, size_t ws_bytes) {
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    return MOE_OK;
 }
 
 }  // namespace
@@ -647,6 +745,271 @@ moe_status moe_fingerprint(const moe_shape *s, const moe_residency *r, const int
     TRY(hip_status(moe::launch_fingerprint(experts, n, r->slot, r->hot_base, r->host_cold, B, s->n_experts, r->n_hot,
                                            r->n_cold, out, static_cast<hipStream_t>(stream)),
                    "fingerprint launch"));
+    return ok();
+}
+
+size_t moe_train_workspace_bytes(const moe_shape *s, int32_t T, int32_t n_seq) {
+    if (check_shape(s) != MOE_OK || check_tokens(T) != MOE_OK || check_seqs(n_seq) != MOE_OK) return 0;
+    size_t n = moe::norm_bwd_ws_bytes(T, s->hidden);
+    const size_t b = moe::balance_ws_bytes(T, s->n_experts, n_seq), r = moe::route_bwd_ws_bytes(T, s->hidden, s->n_experts);
+    n = n > b ? n : b;
+    n = n > r ? n : r;
+    return n > 256 ? n : 256;
+}
+
+moe_status moe_rms_norm(const moe_shape *s, int32_t T, int32_t x_dtype, const void *x, int32_t residual_dtype,
+                        const void *residual, const float *weight, float eps, void *residual_out, uint16_t *y,
+                        int32_t q_kind, uint8_t *q_codes, uint8_t *q_scales, float *rstd, void *stream) {
+    TRY(check_shape(s));
+    TRY(check_tokens(T));
+    TRY(check_dtype(x_dtype, "x_dtype"));
+    if (residual || residual_out) TRY(check_dtype(residual_dtype, "residual_dtype"));
+    if (q_kind != MOE_Q_NONE && q_kind != MOE_Q_OUTPUT && q_kind != MOE_Q_NORMALIZED)
+        return fail(MOE_ERR_INVALID_ARG, "q_kind %d unknown", q_kind);
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps %g must be >= 0 and finite", eps);
+    if (T > 0 && !y && !residual_out && q_kind == MOE_Q_NONE)
+        return fail(MOE_ERR_INVALID_ARG, "no output wanted: y and residual_out are NULL, q_kind is MOE_Q_NONE");
+    if (T == 0) return ok();
+    const size_t n = (size_t)T * s->hidden;
+    ArgCheck c;
+    c.in(x, n * elem_bytes(x_dtype), 16, "x");
+    if (residual) c.in(residual, n * elem_bytes(residual_dtype), 16, "residual");
+    c.in(weight, (size_t)s->hidden * 4, 16, "weight");
+    if (residual_out) c.out(residual_out, n * elem_bytes(residual_dtype), 16, "residual_out");
+    if (y) c.out(y, n * 2, 16, "y");
+    if (q_kind != MOE_Q_NONE) {
+        c.out(q_codes, n, 8, "q_codes");
+        c.out(q_scales, n / 32, 4, "q_scales");
+    }
+    if (rstd) c.out(rstd, (size_t)T * 4, 4, "rstd");
+    c.in_place(residual_out, residual);
+    if (x_dtype == residual_dtype) c.in_place(residual_out, x);
+    if (x_dtype == MOE_OUT_BF16) c.in_place(y, x);
+    TRY(c.status(stream));
+    moe::NormArgs a{};
+    a.T = T;
+    a.H = s->hidden;
+    a.x_dtype = x_dtype;
+    a.res_dtype = residual || residual_out ? residual_dtype : MOE_OUT_F32;   // neither: h = x as it is
+    a.q_kind = q_kind;
+    a.x = x;
+    a.res = residual;
+    a.weight = weight;
+    a.eps = eps;
+    a.res_out = residual_out;
+    a.y = y;
+    a.codes = q_codes;
+    a.scales = q_scales;
+    a.rstd = rstd;
+    TRY(hip_status(moe::launch_rms_norm(a, static_cast<hipStream_t>(stream)), "rms norm launch"));
+    return ok();
+}
+
+moe_status moe_rms_norm_backward(const moe_shape *s, int32_t T, int32_t dy_dtype, const void *dy,
+                                 int32_t dresidual_dtype, const void *dresidual, int32_t h_dtype, const void *h,
+                                 const uint8_t *q_codes, const uint8_t *q_scales, const float *rstd,
+                                 const float *weight, const uint8_t *token_mask, int32_t dx_dtype, void *dx,
+                                 float *dweight, void *ws, size_t ws_bytes, void *stream) {
+    TRY(check_shape(s));
+    TRY(check_tokens(T));
+    TRY(check_dtype(dy_dtype, "dy_dtype"));
+    if (dresidual) TRY(check_dtype(dresidual_dtype, "dresidual_dtype"));
+    if (h) TRY(check_dtype(h_dtype, "h_dtype"));
+    if (dx) TRY(check_dtype(dx_dtype, "dx_dtype"));
+    if (T > 0 && !dx && !dweight) return fail(MOE_ERR_INVALID_ARG, "no output wanted: dx and dweight are NULL");
+    if (T > 0 && h && (q_codes || q_scales))
+        return fail(MOE_ERR_INVALID_ARG, "both h and a checkpoint are given");
+    if (T == 0 && !dweight) return ok();
+    const size_t need = moe::norm_bwd_ws_bytes(T, s->hidden), n = (size_t)T * s->hidden;
+    if (T > 0) TRY(check_train_ws(need, ws_bytes));
+    ArgCheck c;
+    if (T > 0) {
+        c.in(dy, n * elem_bytes(dy_dtype), 16, "dy");
+        if (dresidual) c.in(dresidual, n * elem_bytes(dresidual_dtype), 16, "dresidual");
+        if (h) {
+            c.in(h, n * elem_bytes(h_dtype), 16, "h");
+        } else {
+            c.in(q_codes, n, 8, "q_codes");
+            c.in(q_scales, n / 32, 4, "q_scales");
+        }
+        c.in(rstd, (size_t)T * 4, 4, "rstd");
+        c.in(weight, (size_t)s->hidden * 4, 16, "weight");
+        if (token_mask) c.in(token_mask, (size_t)T, 1, "token_mask");
+        if (dx) c.out(dx, n * elem_bytes(dx_dtype), 16, "dx");
+        c.out(ws, need, 256, "ws");
+        if (dx_dtype == dy_dtype) c.in_place(dx, dy);
+        if (dresidual && dx_dtype == dresidual_dtype) c.in_place(dx, dresidual);
+        if (h && dx_dtype == h_dtype) c.in_place(dx, h);
+    }
+    if (dweight) c.out(dweight, (size_t)s->hidden * 4, 16, "dweight");
+    TRY(c.status(stream));
+    moe::NormBwdArgs a{};
+    a.T = T;
+    a.H = s->hidden;
+    a.dy_dtype = dy_dtype;
+    a.dres_dtype = dresidual ? dresidual_dtype : MOE_OUT_BF16;
+    a.h_dtype = h_dtype;
+    a.dx_dtype = dx ? dx_dtype : MOE_OUT_BF16;
+    a.dy = dy;
+    a.dres = dresidual;
+    a.h = h;
+    a.codes = q_codes;
+    a.scales = q_scales;
+    a.rstd = rstd;
+    a.weight = weight;
+    a.mask = token_mask;
+    a.dx = dx;
+    a.dweight = dweight;
+    TRY(hip_status(moe::launch_rms_norm_backward(a, static_cast<char *>(ws), static_cast<hipStream_t>(stream)),
+                   "rms norm backward launch"));
+    return ok();
+}
+
+static moe::BalanceArgs balance_args(const moe_shape *s, int32_t T, const float *logits, const int32_t *topk_ids,
+                                     const uint8_t *token_mask, const int32_t *seq_offsets, int32_t n_seq,
+                                     float alpha) {
+    moe::BalanceArgs a;
+    a.T = T;
+    a.E = s->n_experts;
+    a.k = s->top_k;
+    a.S = n_seq;
+    a.z = logits;
+    a.ids = topk_ids;
+    a.mask = token_mask;
+    a.offsets = seq_offsets;
+    a.alpha = alpha;
+    return a;
+}
+
+static moe_status check_balance(const moe_shape *s, int32_t T, const int32_t *seq_offsets, int32_t n_seq,
+                                float alpha) {
+    TRY(check_shape(s));
+    TRY(check_tokens(T));
+    TRY(check_seqs(n_seq));
+    if (!seq_offsets && n_seq != 1)
+        return fail(MOE_ERR_INVALID_ARG, "n_seq=%d without seq_offsets (one group needs n_seq = 1)", n_seq);
+    if (!std::isfinite(alpha)) return fail(MOE_ERR_INVALID_ARG, "alpha %g must be finite", alpha);
+    return MOE_OK;
+}
+
+moe_status moe_balance_loss(const moe_shape *s, int32_t T, const float *logits, const int32_t *topk_ids,
+                            const uint8_t *token_mask, const int32_t *seq_offsets, int32_t n_seq, float alpha,
+                            float *loss, int32_t *counts, int32_t *n_valid, float *prob_mean, void *ws,
+                            size_t ws_bytes, void *stream) {
+    TRY(check_balance(s, T, seq_offsets, n_seq, alpha));
+    const size_t E = s->n_experts, need = moe::balance_ws_bytes(T, s->n_experts, n_seq);
+    TRY(check_train_ws(need, ws_bytes));
+    ArgCheck c;
+    if (T > 0) {
+        c.in(logits, (size_t)T * E * 4, 4, "logits");
+        c.in(topk_ids, (size_t)T * s->top_k * 4, 4, "topk_ids");
+        if (token_mask) c.in(token_mask, (size_t)T, 1, "token_mask");
+    }
+    if (seq_offsets) c.in(seq_offsets, ((size_t)n_seq + 1) * 4, 4, "seq_offsets");
+    c.out(loss, 4, 4, "loss");
+    c.out(counts, (size_t)n_seq * E * 4, 4, "counts");
+    c.out(n_valid, ((size_t)n_seq + 1) * 4, 4, "n_valid");
+    if (prob_mean) c.out(prob_mean, (size_t)n_seq * E * 4, 4, "prob_mean");
+    c.out(ws, need, 256, "ws");
+    TRY(c.status(stream));
+    TRY(hip_status(moe::launch_balance_loss(balance_args(s, T, logits, topk_ids, token_mask, seq_offsets, n_seq, alpha),
+                                            loss, counts, n_valid, prob_mean, static_cast<char *>(ws),
+                                            static_cast<hipStream_t>(stream)),
+                   "balance loss launch"));
+    return ok();
+}
+
+moe_status moe_balance_loss_backward(const moe_shape *s, int32_t T, const float *logits, const uint8_t *token_mask,
+                                     const int32_t *seq_offsets, int32_t n_seq, float alpha, const float *dloss,
+                                     const int32_t *counts, const int32_t *n_valid, float *dlogits, void *stream) {
+    TRY(check_balance(s, T, seq_offsets, n_seq, alpha));
+    if (T == 0) return ok();
+    const size_t E = s->n_experts;
+    ArgCheck c;
+    c.in(logits, (size_t)T * E * 4, 4, "logits");
+    if (token_mask) c.in(token_mask, (size_t)T, 1, "token_mask");
+    if (seq_offsets) c.in(seq_offsets, ((size_t)n_seq + 1) * 4, 4, "seq_offsets");
+    if (dloss) c.in(dloss, 4, 4, "dloss");
+    c.in(counts, (size_t)n_seq * E * 4, 4, "counts");
+    c.in(n_valid, ((size_t)n_seq + 1) * 4, 4, "n_valid");
+    c.out(dlogits, (size_t)T * E * 4, 4, "dlogits");
+    c.in_place(dlogits, logits);
+    TRY(c.status(stream));
+    TRY(hip_status(moe::launch_balance_loss_backward(
+                       balance_args(s, T, logits, nullptr, token_mask, seq_offsets, n_seq, alpha), dloss, counts,
+                       n_valid, dlogits, static_cast<hipStream_t>(stream)),
+                   "balance loss backward launch"));
+    return ok();
+}
+
+moe_status moe_route_backward(const moe_shape *s, int32_t T, const uint16_t *x, const uint8_t *q_codes,
+                              const uint8_t *q_scales, const float *q_weight, const float *w_router,
+                              int32_t renormalize, const float *logits, const int32_t *topk_ids, const float *topk_w,
+                              const float *dtopk_w, const float *dlogits_in, const uint8_t *token_mask,
+                              int32_t dx_dtype, void *dx, float *dw_router, float *dbias, void *ws, size_t ws_bytes,
+                              void *stream) {
+    TRY(check_shape(s));
+    TRY(check_tokens(T));
+    if (dx) TRY(check_dtype(dx_dtype, "dx_dtype"));
+    if (T > 0 && !dx && !dw_router && !dbias)
+        return fail(MOE_ERR_INVALID_ARG, "no output wanted: dx, dw_router and dbias are NULL");
+    if (T > 0 && !dtopk_w && !dlogits_in)
+        return fail(MOE_ERR_INVALID_ARG, "no gradient given: dtopk_w and dlogits_in are NULL");
+    if (T > 0 && x && (q_codes || q_scales || q_weight))
+        return fail(MOE_ERR_INVALID_ARG, "both x and a checkpoint are given");
+    if (T == 0 && !dw_router && !dbias) return ok();
+    const size_t H = s->hidden, E = s->n_experts, k = s->top_k, t = T;
+    const size_t need = moe::route_bwd_ws_bytes(T, s->hidden, s->n_experts);
+    if (T > 0) TRY(check_train_ws(need, ws_bytes));
+    ArgCheck c;
+    if (T > 0) {
+        if (dw_router) {
+            if (x) {
+                c.in(x, t * H * 2, 16, "x");
+            } else {
+                c.in(q_codes, t * H, 8, "q_codes");
+                c.in(q_scales, t * H / 32, 4, "q_scales");
+                if (q_weight) c.in(q_weight, H * 4, 16, "q_weight");
+            }
+        }
+        if (dx) c.in(w_router, E * H * 4, 16, "w_router");
+        if (dtopk_w) {
+            c.in(topk_ids, t * k * 4, 4, "topk_ids");
+            c.in(topk_w, t * k * 4, 4, "topk_w");
+            c.in(dtopk_w, t * k * 4, 4, "dtopk_w");
+            if (!renormalize) c.in(logits, t * E * 4, 4, "logits");
+        }
+        if (dlogits_in) c.in(dlogits_in, t * E * 4, 4, "dlogits_in");
+        if (token_mask) c.in(token_mask, t, 1, "token_mask");
+        if (dx) c.out(dx, t * H * elem_bytes(dx_dtype), 16, "dx");
+        c.out(ws, need, 256, "ws");
+    }
+    if (dw_router) c.out(dw_router, E * H * 4, 16, "dw_router");
+    if (dbias) c.out(dbias, E * 4, 4, "dbias");
+    TRY(c.status(stream));
+    moe::RouteBwdArgs a{};
+    a.T = T;
+    a.H = s->hidden;
+    a.E = s->n_experts;
+    a.k = s->top_k;
+    a.renorm = renormalize != 0;
+    a.x = x;
+    a.codes = q_codes;
+    a.scales = q_scales;
+    a.q_weight = q_weight;
+    a.wr = w_router;
+    a.z = logits;
+    a.ids = topk_ids;
+    a.w = topk_w;
+    a.dw = dtopk_w;
+    a.dz_in = dlogits_in;
+    a.mask = token_mask;
+    a.dx_dtype = dx ? dx_dtype : MOE_OUT_BF16;
+    a.dx = dx;
+    a.dwr = dw_router;
+    a.db = dbias;
+    TRY(hip_status(moe::launch_route_backward(a, static_cast<char *>(ws), static_cast<hipStream_t>(stream)),
+                   "router backward launch"));
     return ok();
 }
 

@@ -1,0 +1,328 @@
+// Balance loss over the router's probabilities, per-expert counts, and the
+// gradient with respect to the logits.
+//
+// Tokens form S groups (packed sequences, or one group of all tokens); N_g is
+// group g's number of tokens that count.  With p_t = softmax(z_t):
+//   counts[g][e] = picks of expert e in g,   P[g][e] = sum_t p_t[e] / N_g
+//   f[g][e] = counts E / (k N_g)
+//   loss = alpha / S' sum over the S' groups with N_g > 0 of sum_e f P
+//   dz_t = p_t (a - sum_e p_t a),   a[e] = dloss alpha f[g][e] / (S' N_g)
+// (the counts are piecewise constant: no gradient through them).  A row whose
+// logits are all -inf has p = 0.  Both directions read z once; the backward
+// computes the softmax again instead of storing T x E probabilities.
+#include "train/train.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBalWaves = 8;
+constexpr int kBalThreads = 64 * kBalWaves;
+constexpr int kBalMaxChunks = 1024;
+
+// Tokens per chunk: 32 (four per wave), more where that gave over 1024 chunks.
+int chunk_tokens(int T) {
+    const int n = (T + 32 * kBalMaxChunks - 1) / (32 * kBalMaxChunks);
+    return 32 * (n > 1 ? n : 1);
+}
+
+// Chunk items.  Group g with tokens [o_g, o_{g+1}) gets the items
+// [o_g / R + g, o_{g+1} / R + g + 1): at least ceil(len / R) of them, and a
+// closed form that needs no scan over the groups.
+int chunk_items(int T, int S) { return T / chunk_tokens(T) + S; }
+
+// Group bounds as the kernels use them: inside [0, T] whatever the caller's
+// offsets hold, so a bad table cannot lead outside the arrays.
+__device__ __forceinline__ int bound_of(const int32_t *off, int g, int T) {
+    if (off == nullptr) return g == 0 ? 0 : T;
+    const int v = off[g];
+    return v < 0 ? 0 : (v > T ? T : v);
+}
+
+// Number of g in [1, S) with key(g) <= x (key not decreasing): the index of
+// the group that holds x.
+template <typename F>
+__device__ __forceinline__ int last_group(int S, int x, F key) {
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (key(mid) <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Softmax of one row in the wave: p[i] for expert lane + 64 i.  All -inf: 0.
+template <int NPL>
+__device__ __forceinline__ void row_softmax(const float (&z)[NPL], float (&p)[NPL]) {
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) m = fmaxf(m, z[i]);
+    m = wave_max(m);
+    m = m == -INFINITY ? 0.0f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        p[i] = expf(z[i] - m);
+        s += p[i];
+    }
+    s = wave_sum(s);
+    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) p[i] *= inv;
+}
+
+template <int NPL>
+__device__ __forceinline__ void load_row(const float *zr, int E, float (&z)[NPL]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 64 * i;
+        z[i] = e < E ? zr[e] : -INFINITY;
+    }
+}
+
+struct BalanceWs {
+    float *psum;        // [items][E]
+    int32_t *csum;      // [items][E]
+    int32_t *nsum;      // [items]
+    double *dot;        // [S][column tiles]
+    uint32_t *done;     // finished reduction blocks
+    static size_t layout(int items, int E, int S, char *ws, BalanceWs *o) {
+        size_t at = 0;
+        auto take = [&](size_t n) {
+            const size_t r = at;
+            at += WsLayout::up(n);
+            return ws + r;
+        };
+        BalanceWs w;
+        w.psum = reinterpret_cast<float *>(take((size_t)items * E * 4));
+        w.csum = reinterpret_cast<int32_t *>(take((size_t)items * E * 4));
+        w.nsum = reinterpret_cast<int32_t *>(take((size_t)items * 4));
+        w.dot = reinterpret_cast<double *>(take((size_t)S * ((E + 63) / 64) * 8));
+        w.done = reinterpret_cast<uint32_t *>(take(4));
+        if (o) *o = w;
+        return at;
+    }
+};
+
+// Sums of one chunk: probabilities in registers over the wave's tokens, picks
+// in an LDS histogram (integers: the order of the additions is immaterial).
+template <int NPL>
+__global__ __launch_bounds__(kBalThreads) void balance_sums(BalanceArgs a, int R, BalanceWs w) {
+    __shared__ int hist[kMaxExperts];
+    __shared__ float pl[kBalWaves][64 * NPL];
+    __shared__ int ncount[kBalWaves];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
+    const int item = blockIdx.x;
+    if (item == 0 && tid == 0) *w.done = 0;   // read only by the next launch
+    const auto key = [&](int g) { return bound_of(a.offsets, g, a.T) / R + g; };
+    const int g = a.offsets ? last_group(a.S, item, key) : 0;
+    const int o0 = bound_of(a.offsets, g, a.T), o1 = bound_of(a.offsets, g + 1, a.T);
+    const int chunk = item - key(g);
+    const long long first = o0 + (long long)chunk * R;
+    // chunk < 0: an item before the first group's start
+    const int t0 = chunk >= 0 && first < o1 ? (int)first : o1, t1 = o1 - t0 > R ? t0 + R : o1;
+    for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
+    __syncthreads();
+    float ps[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) ps[i] = 0.f;
+    int n = 0;
+    for (int t = t0 + wave; t < t1; t += kBalWaves) {
+        if (a.mask && a.mask[t] == 0) continue;
+        float z[NPL], p[NPL];
+        load_row<NPL>(a.z + (size_t)t * E, E, z);
+        if (lane < a.k) {
+            const int id = a.ids[(size_t)t * a.k + lane];
+            if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+        }
+        row_softmax<NPL>(z, p);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) ps[i] += p[i];
+        ++n;
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) pl[wave][lane + 64 * i] = ps[i];
+    if (lane == 0) ncount[wave] = n;
+    __syncthreads();
+    for (int e = tid; e < E; e += kBalThreads) {
+        float s[kBalWaves];
+#pragma unroll
+        for (int q = 0; q < kBalWaves; ++q) s[q] = pl[q][e];
+        w.psum[(size_t)item * E + e] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        w.csum[(size_t)item * E + e] = hist[e];
+    }
+    if (tid == 0) {
+        int s = 0;
+        for (int q = 0; q < kBalWaves; ++q) s += ncount[q];
+        w.nsum[item] = s;
+    }
+}
+
+// Sum of the chunk's token counts of group g, by one wave.
+__device__ __forceinline__ int group_tokens(const BalanceWs &w, int i0, int i1) {
+    int n = 0;
+    for (int i = i0 + (int)(threadIdx.x & 63); i < i1; i += 64) n += w.nsum[i];
+    return wave_sum_int(n);
+}
+
+// Block (column tile, group): adds the group's chunks, 64 experts each; the
+// block that finishes last adds the groups' parts of the loss in their order.
+__global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int R, BalanceWs w,
+                                                              float *__restrict__ loss, int32_t *__restrict__ counts,
+                                                              int32_t *__restrict__ n_valid,
+                                                              float *__restrict__ prob_mean) {
+    __shared__ float ps[kBalWaves][64];
+    __shared__ int cs[kBalWaves][64];
+    __shared__ int last;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
+    const int g = blockIdx.y, e = blockIdx.x * 64 + lane, ntile = gridDim.x;
+    const int i0 = bound_of(a.offsets, g, a.T) / R + g, items = a.T / R + a.S;
+    const int i1r = g + 1 < a.S ? bound_of(a.offsets, g + 1, a.T) / R + g + 1 : items;
+    const int i1 = i1r < items ? i1r : items;
+    const int n = group_tokens(w, i0, i1);
+    float p = 0.f;
+    int c = 0;
+    if (e < E)
+        for (int i = i0 + wave; i < i1; i += kBalWaves) {
+            p += w.psum[(size_t)i * E + e];
+            c += w.csum[(size_t)i * E + e];
+        }
+    ps[wave][lane] = p;
+    cs[wave][lane] = c;
+    __syncthreads();
+    if (wave == 0) {
+        float v[kBalWaves];
+        c = 0;
+#pragma unroll
+        for (int q = 0; q < kBalWaves; ++q) {
+            v[q] = ps[q][lane];
+            c += cs[q][lane];
+        }
+        p = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        const float mean = n > 0 ? p / (float)n : 0.0f;
+        if (e < E) {
+            counts[(size_t)g * E + e] = c;
+            if (prob_mean) prob_mean[(size_t)g * E + e] = mean;
+        }
+        const double d = wave_sum_f64(e < E && n > 0 ? (double)c / n * (double)mean : 0.0);
+        if (lane == 0) {
+            w.dot[(size_t)g * ntile + blockIdx.x] = d;
+            if (blockIdx.x == 0) n_valid[g] = n;
+            __threadfence();   // the part is visible before the count says so
+            last = atomicAdd(w.done, 1u) == gridDim.x * gridDim.y - 1;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (wave == 0) {
+        double s = 0.0;
+        int live = 0;
+        for (int q = lane; q < a.S * ntile; q += 64) s += w.dot[q];
+        for (int q = lane; q < a.S; q += 64) live += n_valid[q] > 0;
+        s = wave_sum_f64(s);
+        live = wave_sum_int(live);
+        if (lane == 0) {
+            n_valid[a.S] = live;
+            *loss = live > 0 ? (float)((double)a.alpha * E / a.k * s / live) : 0.0f;
+        }
+    }
+}
+
+// One wave per token at a time; a block takes `rows` consecutive tokens.
+template <int NPL>
+__global__ __launch_bounds__(256) void balance_backward(BalanceArgs a, int rows, const float *__restrict__ dloss,
+                                                        const int32_t *__restrict__ counts,
+                                                        const int32_t *__restrict__ n_valid, float *__restrict__ dz) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = a.E;
+    const int b0 = blockIdx.x * rows;
+    const int b1 = a.T - b0 < rows ? a.T : b0 + rows;
+    const int live = n_valid[a.S];
+    const double up = (double)a.alpha * E / a.k * (dloss ? (double)*dloss : 1.0);
+    int held = -1;
+    float av[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) av[i] = 0.f;
+    for (int t = b0 + wave; t < b1; t += 4) {
+        float *out = dz + (size_t)t * E;
+        int g = 0;
+        bool in = true;
+        if (a.offsets) {
+            g = last_group(a.S, t, [&](int q) { return bound_of(a.offsets, q, a.T); });
+            in = t >= bound_of(a.offsets, g, a.T) && t < bound_of(a.offsets, g + 1, a.T);
+        }
+        if (!in || (a.mask && a.mask[t] == 0)) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (lane + 64 * i < E) out[lane + 64 * i] = 0.f;
+            continue;
+        }
+        float z[NPL], p[NPL];
+        load_row<NPL>(a.z + (size_t)t * E, E, z);
+        if (g != held) {
+            held = g;
+            const double n = n_valid[g];
+            const float f = n > 0 && live > 0 ? (float)(up / (n * n * live)) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int e = lane + 64 * i;
+                av[i] = e < E ? f * (float)counts[(size_t)g * E + e] : 0.0f;
+            }
+        }
+        row_softmax<NPL>(z, p);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s = fmaf(p[i], av[i], s);
+        s = wave_sum(s);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (lane + 64 * i < E) out[lane + 64 * i] = p[i] * (av[i] - s);
+    }
+}
+
+}  // namespace
+
+size_t balance_ws_bytes(int T, int E, int S) {
+    return BalanceWs::layout(chunk_items(T, S), E, S, nullptr, nullptr);
+}
+
+#define MOE_BY_NPL(E, CALL)       \
+    switch (topk_npl(E)) {        \
+        case 1: CALL(1); break;   \
+        case 2: CALL(2); break;   \
+        case 4: CALL(4); break;   \
+        case 8: CALL(8); break;   \
+        default: CALL(16); break; \
+    }
+
+hipError_t launch_balance_loss(const BalanceArgs &a, float *loss, int32_t *counts, int32_t *n_valid, float *prob_mean,
+                               char *ws, hipStream_t st) {
+    const int R = chunk_tokens(a.T), items = chunk_items(a.T, a.S);
+    BalanceWs w;
+    BalanceWs::layout(items, a.E, a.S, ws, &w);
+#define CALL(N) MOE_LAUNCH("balance_sums", balance_sums<N>, dim3(items), dim3(kBalThreads), 0, st, a, R, w)
+    MOE_BY_NPL(a.E, CALL)
+#undef CALL
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    MOE_LAUNCH("balance_reduce", balance_reduce, dim3((a.E + 63) / 64, a.S), dim3(kBalThreads), 0, st, a, R, w, loss,
+               counts, n_valid, prob_mean);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_backward(const BalanceArgs &a, const float *dloss, const int32_t *counts,
+                                        const int32_t *n_valid, float *dz, hipStream_t st) {
+    if (a.T == 0) return hipSuccess;
+    const int rows = a.T <= 4096 ? 4 : 16;
+    const dim3 g((a.T + rows - 1) / rows);
+#define CALL(N) MOE_LAUNCH("balance_backward", balance_backward<N>, g, dim3(256), 0, st, a, rows, dloss, counts, n_valid, dz)
+    MOE_BY_NPL(a.E, CALL)
+#undef CALL
+    return hipGetLastError();
+}
+
+}  // namespace moe

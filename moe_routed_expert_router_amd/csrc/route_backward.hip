@@ -1,0 +1,617 @@
+// Router backward: the gradient of the top-k softmax weights (and of anything
+// else that hands in a gradient of the logits) to the tokens, the router
+// weight and its bias.
+//
+//   renormalised weights (softmax over the k picks):
+//     u_j = w_j (dw_j - sum_i w_i dw_i),    dz[e] = sum over j with id_j = e of u_j
+//   weights of the softmax over all E, p = softmax(z):
+//     dz[e] = p_e (sum over j with id_j = e of dw_j - sum_i w_i dw_i)
+//   plus the caller's dz_in, then
+//     dx = dz Wr,   dWr = dz^T x,   db = sum over tokens of dz.
+//
+// The two products run on the 32x32x16 bf16 MFMA.  dz and Wr are fp32: each
+// is split into bf16 terms (hi + mid + lo carries 24 bits), x is bf16 (or an
+// 8-bit checkpoint, exact in bf16).  dWr takes all three terms of dz (every
+// product exact in fp32, only the accumulation rounds); dx takes hi hi + hi lo
+// + lo hi where it is stored as bf16 (error 2^-16 against the 2^-9 of the
+// store) and the six products above 2^-24 where it is stored as fp32.
+//
+// Operand layout.  The launches before the products write every operand as
+// units of 1 KB in the MFMA's own lane order: a unit holds 32 rows x 16 values
+// of the contraction, lane l's eight (row l % 32, contraction 8 (l / 32) ..
+// +7) at byte 16 l.  A unit goes to LDS as one linear copy and to registers
+// as one conflict-free 16-byte read per lane.
+#include "train/train.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kUnit = 1024;   // bytes of an operand unit
+constexpr int kDzTok = 32;    // tokens per block of route_dz
+
+// ------------------------------- workspace ---------------------------------
+struct RouteWs {
+    int tg, ec, eg, hg;   // groups: 32 tokens, 16 experts (even), 32 experts, 32 hidden columns
+    size_t dza, dzt, wrp, dbp, dwp, total;
+    int splits;
+};
+
+constexpr int kTileE = 128, kTileH = 128, kTileT = 128;
+constexpr int kStepK = 32;
+constexpr int kMaxSplits = 16;
+
+// Token splits of the dWr product: as many as bring the (expert, hidden)
+// tiles to about 512 blocks (two per CU), each with at least 8 steps of 32
+// tokens, at most kMaxSplits (every split writes and re-reads a partial dWr).
+int dw_splits(int T, int H, int E) {
+    const int tiles = ((E + kTileE - 1) / kTileE) * ((H + kTileH - 1) / kTileH);
+    int s = 512 / tiles;
+    const int most = (T + 8 * kStepK - 1) / (8 * kStepK);
+    s = s < most ? s : most;
+    return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
+}
+
+RouteWs route_ws(int T, int H, int E, int planes) {
+    RouteWs w;
+    w.tg = (T + 31) / 32;
+    w.eg = (E + 31) / 32;
+    w.ec = 2 * w.eg;
+    w.hg = H / 32;
+    w.splits = dw_splits(T, H, E);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t r = at;
+        at += WsLayout::up(n);
+        return r;
+    };
+    w.dza = take((size_t)w.tg * w.ec * planes * kUnit);
+    w.dzt = take((size_t)w.tg * 2 * w.eg * 3 * kUnit);
+    w.wrp = take((size_t)w.hg * w.ec * planes * kUnit);
+    w.dbp = take((size_t)w.tg * E * 4);
+    w.dwp = take((size_t)w.splits * E * H * 4);
+    w.total = at;
+    return w;
+}
+
+// ------------------------------- bf16 terms --------------------------------
+// v = t[0] + t[1] (+ t[2]) with bf16 terms, each the nearest to what is left.
+template <int NP>
+__device__ __forceinline__ void split_terms(float v, uint32_t *t) {
+    float r = v;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const __bf16 h = (__bf16)r;
+        t[p] = __builtin_bit_cast(uint16_t, h);
+        r = r - (float)h;
+    }
+    // an infinity (or a value that rounds to one) would leave NaN terms
+    // behind: the first term alone carries it
+    if ((t[0] & 0x7f80u) == 0x7f80u) {
+#pragma unroll
+        for (int p = 1; p < NP; ++p) t[p] = 0;
+    }
+}
+
+// Eight values as NP units' 16-byte pieces.
+template <int NP>
+__device__ __forceinline__ void split8(const float *v, uint4 *o) {
+    uint32_t w[NP][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a[NP], b[NP];
+        split_terms<NP>(v[2 * i], a);
+        split_terms<NP>(v[2 * i + 1], b);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) w[p][i] = a[p] | (b[p] << 16);
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) o[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// --------------------------------- dz --------------------------------------
+// 32 tokens per block, one wave per token at a time: dz of the row in
+// registers, then in an LDS tile from which it leaves in both operand orders
+// (token rows for dx, expert rows for dWr) and as the block's part of db.
+// Tokens past T and masked tokens have dz = 0.
+template <int NPL, int NP>
+__global__ __launch_bounds__(512) void route_dz(RouteBwdArgs a, uint8_t *__restrict__ dza, uint8_t *__restrict__ dzt,
+                                                float *__restrict__ dbp, int EC, int EG) {
+    constexpr int kPitch = 64 * NPL + 4;
+    __shared__ __align__(16) float tile[kDzTok][kPitch];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E, k = a.k;
+    const int tgrp = blockIdx.x, tok0 = tgrp * kDzTok;
+    for (int r = wave; r < kDzTok; r += 8) {
+        const int t = tok0 + r;
+        float v[NPL];
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) v[i] = 0.f;
+        if (t < a.T && !(a.mask && a.mask[t] == 0)) {
+            const size_t at = (size_t)t * E;
+            if (a.dz_in) {
+#pragma unroll
+                for (int i = 0; i < NPL; ++i)
+                    if (lane + 64 * i < E) v[i] = a.dz_in[at + lane + 64 * i];
+            }
+            if (a.dw) {
+                int id = -1;
+                float w = 0.f, d = 0.f;
+                if (lane < k) {
+                    id = a.ids[(size_t)t * k + lane];
+                    w = a.w[(size_t)t * k + lane];
+                    d = a.dw[(size_t)t * k + lane];
+                }
+                if (id < 0 || id >= E) id = -1;
+                // a pick outside [0, E) added nothing to the output: its weight has no gradient
+                const float dot = wave_sum(id >= 0 ? w * d : 0.f);
+                if (a.renorm) {
+                    const float u = w * ((id >= 0 ? d : 0.f) - dot);
+                    for (int j = 0; j < k; ++j) {
+                        const int ej = __builtin_amdgcn_readlane(id, j);
+                        const float uj = readlanef(u, j);
+#pragma unroll
+                        for (int i = 0; i < NPL; ++i)
+                            if (lane + 64 * i == ej) v[i] += uj;
+                    }
+                } else {
+                    float z[NPL], m = -INFINITY, s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i) {
+                        const int e = lane + 64 * i;
+                        z[i] = e < E ? a.z[at + e] : -INFINITY;
+                        z[i] = z[i] == z[i] ? z[i] : -INFINITY;   // as the forward: NaN is left out of the sum
+                        m = fmaxf(m, z[i]);
+                    }
+                    m = wave_max(m);
+                    m = m == -INFINITY ? 0.f : m;
+                    float g[NPL];
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i) {
+                        z[i] = expf(z[i] - m);
+                        s += z[i];
+                        g[i] = -dot;
+                    }
+                    s = wave_sum(s);
+                    const float inv = s == 0.f ? 0.f : 1.f / s;
+                    for (int j = 0; j < k; ++j) {
+                        const int ej = __builtin_amdgcn_readlane(id, j);
+                        const float dj = readlanef(d, j);
+#pragma unroll
+                        for (int i = 0; i < NPL; ++i)
+                            if (lane + 64 * i == ej) g[i] += dj;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i) v[i] = fmaf(z[i] * inv, g[i], v[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) tile[r][lane + 64 * i] = v[i];
+    }
+    __syncthreads();
+    if (dbp) {
+        for (int e = tid; e < E; e += 512) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int r = 0; r < kDzTok; ++r) s[r & 3] += tile[r][e];
+            dbp[(size_t)tgrp * E + e] = (s[0] + s[1]) + (s[2] + s[3]);
+        }
+    }
+    // token rows: the 16-expert chunk ec of this token group, lane (token
+    // l % 32, experts 8 (l / 32) .. +7); columns E .. 16 EC - 1 of the tile are 0
+    if (dza) {
+        for (int ec = wave; ec < EC; ec += 8) {
+            const float *p = &tile[lane & 31][16 * ec + 8 * (lane >> 5)];
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = p[i];
+            uint4 o[NP];
+            split8<NP>(v, o);
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+                *reinterpret_cast<uint4 *>(dza + (((size_t)tgrp * EC + ec) * NP + q) * kUnit + 16 * lane) = o[q];
+        }
+    }
+    // expert rows: units (16-token chunk, 32 experts), lane (expert l % 32,
+    // tokens 8 (l / 32) .. +7)
+    if (dzt) {
+        for (int u = wave; u < 2 * EG; u += 8) {
+            const int half = u / EG, eg = u - half * EG;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = tile[16 * half + 8 * (lane >> 5) + i][32 * eg + (lane & 31)];
+            uint4 o[3];
+            split8<3>(v, o);
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                *reinterpret_cast<uint4 *>(dzt + (((size_t)(2 * tgrp + half) * EG + eg) * 3 + q) * kUnit + 16 * lane) =
+                    o[q];
+        }
+    }
+}
+
+// ----------------------------- router weight -------------------------------
+// Wr [E][H] as units (32 hidden columns, 16 experts): block = 64 columns of
+// one 32-expert group, through an LDS tile.
+template <int NP>
+__global__ __launch_bounds__(256) void route_wr_units(const float *__restrict__ wr, int E, int H,
+                                                      uint8_t *__restrict__ out, int EC) {
+    __shared__ float tile[32][65];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int h0 = blockIdx.x * 64, e0 = blockIdx.y * 32;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const int e = e0 + wave * 8 + r;
+        tile[wave * 8 + r][lane] = e < E ? wr[(size_t)e * H + h0 + lane] : 0.f;
+    }
+    __syncthreads();
+    const int hg = wave >> 1, ch = wave & 1;   // a wave: one unit
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = tile[16 * ch + 8 * (lane >> 5) + i][32 * hg + (lane & 31)];
+    uint4 o[NP];
+    split8<NP>(v, o);
+    const size_t unit = (size_t)(2 * blockIdx.x + hg) * EC + 2 * blockIdx.y + ch;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint4 *>(out + (unit * NP + q) * kUnit + 16 * lane) = o[q];
+}
+
+// ----------------------------------- dx ------------------------------------
+__device__ __forceinline__ bf16x8 lds_unit(const uint8_t *p) {
+    return *reinterpret_cast<const bf16x8 *>(p + 16 * (threadIdx.x & 63));
+}
+
+// One linear copy of a unit into LDS by this wave.
+__device__ __forceinline__ void fill_unit(const uint8_t *src, uint8_t *dst) {
+    lds_fill<16>(buffer_rsrc(src, kUnit), 16 * (threadIdx.x & 63), dst);
+}
+
+// dx tile: 128 tokens x 128 hidden columns, contraction over the experts in
+// steps of 32; four waves of 64 x 64.  MFMA rows = hidden columns, columns =
+// tokens: a lane ends with four consecutive columns of one token.
+template <int NP, typename DX>
+__global__ __launch_bounds__(256) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp, int T,
+                                                int H, int EC, int TG, void *__restrict__ dx) {
+    constexpr int kOp = 4 * 2 * NP * kUnit;   // one operand's share of a stage
+    __shared__ __align__(1024) uint8_t st0[2 * kOp];
+    __shared__ __align__(1024) uint8_t st1[2 * kOp];
+    const int HT = H / kTileH, hper = (HT + 7) / 8;
+    const int xcd = blockIdx.x & 7, rest = blockIdx.x >> 3;
+    const int ht = xcd * hper + rest % hper, tt = rest / hper;
+    if (ht >= HT) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int HG = H / 32, S = EC / 2;
+    // fills: wave w copies group w of each operand (2 chunks x NP units)
+    const int tgrp = 4 * tt + wave < TG ? 4 * tt + wave : TG - 1;
+    const uint8_t *asrc = wrp + (size_t)(4 * ht + wave < HG ? 4 * ht + wave : HG - 1) * EC * NP * kUnit;
+    const uint8_t *bsrc = dza + (size_t)tgrp * EC * NP * kUnit;
+    auto fill = [&](uint8_t *st, int s) {
+#pragma unroll
+        for (int u = 0; u < 2 * NP; ++u) {
+            fill_unit(asrc + ((size_t)s * 2 * NP + u) * kUnit, st + (wave * 2 * NP + u) * kUnit);
+            fill_unit(bsrc + ((size_t)s * 2 * NP + u) * kUnit, st + kOp + (wave * 2 * NP + u) * kUnit);
+        }
+    };
+    const int wr = wave & 1, wc = wave >> 1;   // this wave's 64 hidden columns and 64 tokens
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    auto step = [&](const uint8_t *cur) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            bf16x8 A[2][NP], B[2][NP];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    A[i][p] = lds_unit(cur + (((2 * wr + i) * 2 + c) * NP + p) * kUnit);
+                    B[i][p] = lds_unit(cur + kOp + (((2 * wc + i) * 2 + c) * NP + p) * kUnit);
+                }
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int q = 0; q < NP - p; ++q)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[i][p], B[j][q], acc[i][j]);
+        }
+    };
+    fill(st0, 0);
+    for (int s = 0; s < S; s += 2) {
+        wait_vmem();
+        __syncthreads();
+        if (s + 1 < S) fill(st1, s + 1);
+        step(st0);
+        if (s + 1 >= S) break;
+        wait_vmem();
+        __syncthreads();
+        if (s + 2 < S) fill(st0, s + 2);
+        step(st1);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int t = kTileT * tt + 64 * wc + 32 * j + (lane & 31);
+        if (t >= T) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
+                const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
+                            v3 = acc[i][j][4 * q + 3];
+                const size_t at = (size_t)t * H + h;
+                if constexpr (__is_same(DX, float))
+                    *reinterpret_cast<float4 *>(static_cast<float *>(dx) + at) = make_float4(v0, v1, v2, v3);
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dx) + at) =
+                        make_uint2(bf16x2_bits(v0, v1), bf16x2_bits(v2, v3));
+            }
+    }
+}
+
+// ----------------------------------- dWr -----------------------------------
+// Tokens of one thread's piece of a step: two hidden columns x eight tokens,
+// as two bf16 per dword (x) or two codes and their scale (checkpoint).
+template <bool MX>
+struct XPiece {
+    uint32_t v[8];
+    uint32_t s[MX ? 8 : 1];
+    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, int t1, int h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + i;
+            const bool in = t < t1 && !(a.mask && a.mask[t] == 0);   // past the end or masked: 0 whatever is stored
+            const size_t at = (size_t)(in ? t : 0) * a.H + h;
+            if constexpr (MX) {
+                const uint32_t c = *reinterpret_cast<const uint16_t *>(a.codes + at);
+                const uint32_t sc = a.scales[at >> 5];
+                v[i] = in ? c : 0u;
+                s[i] = in ? sc : 127u;
+            } else {
+                const uint32_t c = *reinterpret_cast<const uint32_t *>(a.x + at);
+                v[i] = in ? c : 0u;
+            }
+        }
+    }
+    // the eight tokens of column h (lo) and h + 1 (hi) as 16-byte pieces
+    __device__ __forceinline__ void pieces(uint4 &lo, uint4 &hi) {
+        uint32_t d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (MX) {
+                typedef float f2 __attribute__((ext_vector_type(2)));
+                const f2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[i], false);
+                const float sc = e8m0_to_f32(s[i]);
+                d[i] = bf16x2_bits(f[0] * sc, f[1] * sc);
+            } else {
+                d[i] = v[i];
+            }
+        }
+        uint32_t l[4], u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            l[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x05040100u);
+            u[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x07060302u);
+        }
+        lo = make_uint4(l[0], l[1], l[2], l[3]);
+        hi = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+
+// 16-byte slot s of a unit of x sits at slot s ^ ((s >> 3) & 1): a wave
+// writing the slots 2 l (then 2 l + 1) hits every bank group once per 8 lanes.
+__device__ __forceinline__ int x_slot(int s) { return 16 * (s ^ ((s >> 3) & 1)); }
+
+// dWr tile: 128 experts x 128 hidden columns over one split of the tokens in
+// steps of 32.  MFMA rows = experts (dz units, copied to LDS), columns =
+// hidden columns (x, transposed in registers on its way to LDS).
+// out: the split's partial [E][H], or dWr itself with one split.
+template <bool MX>
+__global__ __launch_bounds__(256) void route_dwr(RouteBwdArgs a, const uint8_t *__restrict__ dzt, int EG, int steps,
+                                                 int splits, float *__restrict__ out) {
+    constexpr int kA = 4 * 2 * 3 * kUnit, kB = 4 * 2 * kUnit;
+    __shared__ __align__(1024) uint8_t st0[kA + kB];
+    __shared__ __align__(1024) uint8_t st1[kA + kB];
+    const int H = a.H, E = a.E;
+    const int net = (E + kTileE - 1) / kTileE;
+    const int nht = H / kTileH;
+    // the expert tiles of one (split, hidden tile) are consecutive on one XCD
+    // (they read the same x), and an XCD stays with few splits (the same dz)
+    const int total = net * nht * splits, per = (total + 7) / 8;
+    const int idx = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || idx >= total) return;
+    const int et = idx % net, ht = (idx / net) % nht, sp = idx / (net * nht);
+    const int per_split = (steps + splits - 1) / splits;
+    const int s0 = sp * per_split, s1 = s0 + per_split < steps ? s0 + per_split : steps;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int eg = 4 * et + wave < EG ? 4 * et + wave : EG - 1;
+    auto fill_a = [&](uint8_t *st, int s) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                fill_unit(dzt + (((size_t)(2 * s + c) * EG + eg) * 3 + p) * kUnit,
+                          st + ((wave * 2 + c) * 3 + p) * kUnit);
+    };
+    // x piece of this thread: hidden columns 2 lane, 2 lane + 1 of the tile,
+    // tokens 8 wave .. +7 of the step (chunk wave / 2, lane half wave % 2)
+    const int h = kTileH * ht + 2 * lane;
+    uint8_t *const xdst0 = st0 + kA, *const xdst1 = st1 + kA;
+    const int xunit = ((lane >> 4) * 2 + (wave >> 1)) * kUnit;
+    const int slot = ((2 * lane) & 31) + 32 * (wave & 1);
+    auto put_x = [&](uint8_t *dst, XPiece<MX> &x) {
+        uint4 lo, hi;
+        x.pieces(lo, hi);
+        *reinterpret_cast<uint4 *>(dst + xunit + x_slot(slot)) = lo;
+        *reinterpret_cast<uint4 *>(dst + xunit + x_slot(slot + 1)) = hi;
+    };
+    const int wr = wave & 1, wc = wave >> 1;   // this wave's 64 experts and 64 hidden columns
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    auto step = [&](const uint8_t *cur) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            bf16x8 A[2][3], B[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int p = 0; p < 3; ++p) A[i][p] = lds_unit(cur + (((2 * wr + i) * 2 + c) * 3 + p) * kUnit);
+                B[i] = *reinterpret_cast<const bf16x8 *>(cur + kA + ((2 * wc + i) * 2 + c) * kUnit + x_slot(lane));
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[i][p], B[j], acc[i][j]);
+        }
+    };
+    XPiece<MX> x;
+    if (s0 < s1) {
+        fill_a(st0, s0);
+        x.load(a, kStepK * s0 + 8 * wave, a.T, h);
+        put_x(xdst0, x);
+    }
+    for (int s = s0; s < s1; s += 2) {
+        wait_vmem();
+        __syncthreads();
+        if (s + 1 < s1) {
+            fill_a(st1, s + 1);
+            x.load(a, kStepK * (s + 1) + 8 * wave, a.T, h);
+        }
+        step(st0);
+        if (s + 1 >= s1) break;
+        put_x(xdst1, x);
+        wait_vmem();
+        __syncthreads();
+        if (s + 2 < s1) {
+            fill_a(st0, s + 2);
+            x.load(a, kStepK * (s + 2) + 8 * wave, a.T, h);
+        }
+        step(st1);
+        if (s + 2 < s1) put_x(xdst0, x);
+    }
+    float *const dst = out + (splits > 1 ? (size_t)sp * E * H : 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int hc = kTileH * ht + 64 * wc + 32 * j + (lane & 31);
+        const float sc = splits == 1 && a.q_weight ? a.q_weight[hc] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int e = kTileE * et + 64 * wr + 32 * i + 8 * (q / 4) + 4 * (lane >> 5) + q % 4;
+                if (e < E) dst[(size_t)e * H + hc] = acc[i][j][q] * sc;
+            }
+    }
+}
+
+// dWr from the splits' partials, in split order, times the checkpoint's column weight.
+__global__ __launch_bounds__(256) void route_dwr_sum(const float4 *__restrict__ part, int splits, size_t n4, int H4,
+                                                     const float4 *__restrict__ q_weight, float4 *__restrict__ out) {
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    float4 s = part[i];
+    for (int p = 1; p < splits; ++p) {
+        const float4 v = part[(size_t)p * n4 + i];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    if (q_weight) {
+        const float4 w = q_weight[i % H4];
+        s.x *= w.x;
+        s.y *= w.y;
+        s.z *= w.z;
+        s.w *= w.w;
+    }
+    out[i] = s;
+}
+
+// Zeros (a kernel, so that the call may be captured in a graph).
+__global__ __launch_bounds__(256) void route_zero(float *p, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0.f;
+}
+
+template <int NP>
+void launch_dz(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
+    uint8_t *dza = a.dx ? reinterpret_cast<uint8_t *>(ws + w.dza) : nullptr;
+    uint8_t *dzt = a.dwr ? reinterpret_cast<uint8_t *>(ws + w.dzt) : nullptr;
+    float *dbp = a.db ? reinterpret_cast<float *>(ws + w.dbp) : nullptr;
+    const dim3 g(w.tg), b(512);
+#define MOE_DZ(N) MOE_LAUNCH("route_dz", (route_dz<N, NP>), g, b, 0, st, a, dza, dzt, dbp, w.ec, w.eg)
+    switch (topk_npl(a.E)) {
+        case 1: MOE_DZ(1); break;
+        case 2: MOE_DZ(2); break;
+        case 4: MOE_DZ(4); break;
+        case 8: MOE_DZ(8); break;
+        default: MOE_DZ(16); break;
+    }
+#undef MOE_DZ
+}
+
+template <int NP, typename DX>
+void launch_dx(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
+    uint8_t *wrp = reinterpret_cast<uint8_t *>(ws + w.wrp);
+    MOE_LAUNCH("route_wr_units", route_wr_units<NP>, dim3(a.H / 64, w.eg), dim3(256), 0, st, a.wr, a.E, a.H, wrp, w.ec);
+    const int hper = (a.H / kTileH + 7) / 8, tt = (a.T + kTileT - 1) / kTileT;
+    MOE_LAUNCH("route_dx", (route_dx<NP, DX>), dim3(8 * hper * tt), dim3(256), 0, st,
+               reinterpret_cast<const uint8_t *>(ws + w.dza), wrp, a.T, a.H, w.ec, w.tg, a.dx);
+}
+
+}  // namespace
+
+size_t route_bwd_ws_bytes(int T, int H, int E) { return route_ws(T, H, E, 3).total; }
+
+hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st) {
+    const int planes = a.dx_dtype == MOE_OUT_F32 ? 3 : 2;
+    const RouteWs w = route_ws(a.T, a.H, a.E, planes);
+    const size_t ne = (size_t)a.E * a.H;
+    if (a.T == 0) {
+        if (a.dwr) MOE_LAUNCH("route_zero", route_zero, dim3(512), dim3(256), 0, st, a.dwr, ne);
+        if (a.db) MOE_LAUNCH("route_zero", route_zero, dim3(1), dim3(256), 0, st, a.db, (size_t)a.E);
+        return hipGetLastError();
+    }
+    if (planes == 3)
+        launch_dz<3>(a, w, ws, st);
+    else
+        launch_dz<2>(a, w, ws, st);
+    if (a.dx) {
+        if (planes == 3)
+            launch_dx<3, float>(a, w, ws, st);
+        else
+            launch_dx<2, Bf16>(a, w, ws, st);
+    }
+    if (a.dwr) {
+        const uint8_t *dzt = reinterpret_cast<const uint8_t *>(ws + w.dzt);
+        float *part = reinterpret_cast<float *>(ws + w.dwp);
+        float *out = w.splits > 1 ? part : a.dwr;
+        const int total = ((a.E + kTileE - 1) / kTileE) * (a.H / kTileH) * w.splits;
+        const dim3 g(8 * ((total + 7) / 8));
+        if (a.x == nullptr)
+            MOE_LAUNCH("route_dwr", route_dwr<true>, g, dim3(256), 0, st, a, dzt, w.eg, w.tg, w.splits, out);
+        else
+            MOE_LAUNCH("route_dwr", route_dwr<false>, g, dim3(256), 0, st, a, dzt, w.eg, w.tg, w.splits, out);
+        if (w.splits > 1) {
+            const size_t n4 = ne / 4;
+            MOE_LAUNCH("route_dwr_sum", route_dwr_sum, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st,
+                       reinterpret_cast<const float4 *>(part), w.splits, n4, a.H / 4,
+                       reinterpret_cast<const float4 *>(a.q_weight), reinterpret_cast<float4 *>(a.dwr));
+        }
+    }
+    if (a.db) return launch_column_sum("db_sum", reinterpret_cast<const float *>(ws + w.dbp), w.tg, a.E, a.db, st);
+    return hipGetLastError();
+}
+
+}  // namespace moe

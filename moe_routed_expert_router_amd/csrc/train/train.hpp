@@ -1,0 +1,188 @@
+// Launchers and shared device code of the norm and of the router's training
+// side (norm.hip, balance.hip, route_backward.hip).  In a folder of its own:
+// the layer's forward kernels do not depend on it.
+#pragma once
+
+#include "../device_util.hpp"
+#include "../kernels.hpp"
+
+namespace moe {
+
+// ------------------------------- launchers ---------------------------------
+// dtype arguments: MOE_OUT_F32 or MOE_OUT_BF16.
+struct NormArgs {
+    int T, H;
+    int x_dtype, res_dtype, q_kind;
+    const void *x;
+    const void *res;      // null: h = x
+    const float *weight;
+    float eps;
+    void *res_out;        // null: not written
+    uint16_t *y;          // null: not written
+    uint8_t *codes, *scales;
+    float *rstd;          // null: not written
+};
+hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st);
+
+struct NormBwdArgs {
+    int T, H;
+    int dy_dtype, dres_dtype, h_dtype, dx_dtype;
+    const void *dy;
+    const void *dres;     // null: none
+    const void *h;        // null: from codes / scales
+    const uint8_t *codes, *scales;
+    const float *rstd, *weight;
+    const uint8_t *mask;  // null: every token counts
+    void *dx;             // null: not written
+    float *dweight;       // null: not written
+};
+size_t norm_bwd_ws_bytes(int T, int H);
+hipError_t launch_rms_norm_backward(const NormBwdArgs &a, char *ws, hipStream_t st);
+
+struct BalanceArgs {
+    int T, E, k, S;
+    const float *z;
+    const int32_t *ids;
+    const uint8_t *mask;      // null: every token counts
+    const int32_t *offsets;   // null: one group of all tokens
+    float alpha;
+};
+size_t balance_ws_bytes(int T, int E, int S);
+hipError_t launch_balance_loss(const BalanceArgs &a, float *loss, int32_t *counts, int32_t *n_valid, float *prob_mean,
+                               char *ws, hipStream_t st);
+hipError_t launch_balance_loss_backward(const BalanceArgs &a, const float *dloss, const int32_t *counts,
+                                        const int32_t *n_valid, float *dz, hipStream_t st);
+
+struct RouteBwdArgs {
+    int T, H, E, k, renorm;
+    const uint16_t *x;                    // null: from codes / scales
+    const uint8_t *codes, *scales;
+    const float *q_weight;                // null: 1
+    const float *wr;
+    const float *z;                       // read when !renorm
+    const int32_t *ids;
+    const float *w, *dw;                  // dw null: no gradient of the weights
+    const float *dz_in;                   // null: none
+    const uint8_t *mask;                  // null: every token counts
+    int dx_dtype;
+    void *dx;                             // null: not written
+    float *dwr, *db;                      // null: not written
+};
+size_t route_bwd_ws_bytes(int T, int H, int E);
+hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st);
+
+// out[c] = sum over r of part[r][c] in row order of four interleaved chains
+// (fixed for a given R); part [R][C].  R = 0 writes zeros.
+hipError_t launch_column_sum(const char *name, const float *part, int R, int C, float *out, hipStream_t st);
+
+// ------------------------------ device code --------------------------------
+struct Bf16 {};   // tag: 16-bit storage
+struct Mx8 {};    // tag: e4m3 codes with an e8m0 scale per 32
+
+// Eight consecutive elements as loaded (unpacked where they are used, so a
+// row's loads are all issued before the first wait).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void *p, size_t i) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        a = q[0];
+        b = q[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float *v) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+template <>
+struct Raw8<Bf16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const void *p, size_t i) {
+        a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float *v) const {
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Raw8<Mx8> {
+    uint2 a;
+    uint32_t s;
+    __device__ __forceinline__ void load2(const uint8_t *codes, const uint8_t *scales, size_t i) {
+        a = *reinterpret_cast<const uint2 *>(codes + i);
+        s = scales[i >> 5];
+    }
+    __device__ __forceinline__ void zero() {
+        a = make_uint2(0u, 0u);
+        s = 127;
+    }
+    // the values the codes stand for (exact: four significant bits)
+    __device__ __forceinline__ void get(float *v) const {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const float sc = e8m0_to_f32(s);
+        const f2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.x, false);
+        const f2 p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.x, true);
+        const f2 p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.y, false);
+        const f2 p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.y, true);
+        v[0] = p0[0] * sc; v[1] = p0[1] * sc; v[2] = p1[0] * sc; v[3] = p1[1] * sc;
+        v[4] = p2[0] * sc; v[5] = p2[1] * sc; v[6] = p3[0] * sc; v[7] = p3[1] * sc;
+    }
+};
+
+// Two values as bf16 bits (round to nearest even; a in the low half).
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+    bf16x2 r;
+    r[0] = (__bf16)a;
+    r[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ void store8(float, void *p, size_t i, const float *v) {
+    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(Bf16, void *p, size_t i, const float *v) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(
+        bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+}
+
+// Sum of a double over the wave, the same bits in every lane.
+template <int CTRL>
+__device__ __forceinline__ double dpp_movd(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)dpp_mov<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp_mov<CTRL>((int)(u >> 32));
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double readlaned(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v += dpp_movd<kDppXor1>(v);
+    v += dpp_movd<kDppXor2>(v);
+    v += dpp_movd<kDppHalfMirror>(v);
+    v += dpp_movd<kDppMirror>(v);
+    return (readlaned(v, 0) + readlaned(v, 16)) + (readlaned(v, 32) + readlaned(v, 48));
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, dpp_movf<kDppXor1>(v));
+    v = fmaxf(v, dpp_movf<kDppXor2>(v));
+    v = fmaxf(v, dpp_movf<kDppHalfMirror>(v));
+    v = fmaxf(v, dpp_movf<kDppMirror>(v));
+    return fmaxf(fmaxf(readlanef(v, 0), readlanef(v, 16)), fmaxf(readlanef(v, 32), readlanef(v, 48)));
+}
+
+}  // namespace moe
