@@ -11,6 +11,15 @@ import ctypes
 import os
 from ctypes import c_float, c_int32, c_size_t, c_void_p, c_char_p, POINTER
 
+# One HIP runtime per process.  torch ships its own copy of the runtime (same
+# soname as the system one libmoe.so links); loaded before it, it also serves
+# the library.  The other order would put two runtimes in the process, and
+# torch's device memory would be unknown to the library's.
+try:
+    import torch
+except ImportError:
+    torch = None
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
@@ -57,14 +66,6 @@ class MoeResidency(ctypes.Structure):
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run python moe_routed_expert_router_amd/build.py")
-    # One HIP runtime per process.  torch ships its own copy of the runtime
-    # (same soname as the system one this library links); loaded first, it
-    # also serves this library.  The other order would put two runtimes in the
-    # process, and torch's device memory would be unknown to the library's.
-    try:
-        import torch  # noqa: F401
-    except ImportError:
-        pass
     lib = ctypes.CDLL(LIB_PATH)
     P = c_void_p
     sig = {
@@ -133,9 +134,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch is not None else None
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
+        # the raw handle where torch hands it out: building a Stream object
+        # costs 3 us, as much as a launch
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -286,28 +293,30 @@ def moe_fingerprint(s: MoeShape, r: MoeResidency, experts, out, stream=None) -> 
 # ------------------ the norm and the router's training side ------------------
 # Tensors are checked here for type, shape and contiguity (the C entries see
 # addresses only); None stands for NULL.
-def _codes_types():
-    """Types of 8-bit codes and of their scales: bytes, or torch's own types of the same bits."""
-    import torch
-    return (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
-
-
-def _fit(name: str, t, shape: tuple, *dtypes):
+def _fit(name: str, t, shape: tuple, dtypes: tuple):
     if t is None:
         return None
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+if torch is not None:
+    _F32, _I32, _B16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+    _REAL = (torch.bfloat16, torch.float32)
+    _BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+    _MASK = (torch.uint8, torch.bool)
+    # 8-bit codes and their scales: bytes, or torch's own types of the same bits
+    _CODES, _SCALES = (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
 
 
 def _kind(t) -> int:
     """moe_out_dtype of a tensor that _fit accepted (None: unused)."""
-    import torch
-    return MOE_OUT_F32 if t is not None and t.dtype == torch.float32 else MOE_OUT_BF16
+    return MOE_OUT_F32 if t is not None and t.dtype is torch.float32 else MOE_OUT_BF16
 
 
 def _ws(ws) -> tuple:
@@ -322,14 +331,11 @@ def moe_rms_norm(s: MoeShape, x, residual, weight, eps: float, residual_out, y, 
                  q_codes=None, q_scales=None, rstd=None, stream=None) -> None:
     """h = x + residual -> residual_out; y = h r weight (bf16); the 8-bit
     output by q_kind; rstd = r.  x and the residual are float32 or bfloat16."""
-    import torch
     T, H = x.shape[0], s.hidden
-    f32, b16 = torch.float32, torch.bfloat16
-    ct, st = _codes_types()
-    p = (_fit("x", x, (T, H), f32, b16), _fit("residual", residual, (T, H), f32, b16),
-         _fit("weight", weight, (H,), f32), _fit("residual_out", residual_out, (T, H), f32, b16),
-         _fit("y", y, (T, H), b16), _fit("q_codes", q_codes, (T, H), *ct),
-         _fit("q_scales", q_scales, (T, H // 32), *st), _fit("rstd", rstd, (T,), f32))
+    p = (_fit("x", x, (T, H), _REAL), _fit("residual", residual, (T, H), _REAL),
+         _fit("weight", weight, (H,), _F32), _fit("residual_out", residual_out, (T, H), _REAL),
+         _fit("y", y, (T, H), _B16), _fit("q_codes", q_codes, (T, H), _CODES),
+         _fit("q_scales", q_scales, (T, H // 32), _SCALES), _fit("rstd", rstd, (T,), _F32))
     if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
         raise TypeError(f"residual is {residual.dtype} and residual_out {residual_out.dtype}: they must agree")
     _check(lib.moe_rms_norm(ctypes.byref(s), T, _kind(x), p[0], _kind(residual if residual_out is None else residual_out),
@@ -339,15 +345,12 @@ def moe_rms_norm(s: MoeShape, x, residual, weight, eps: float, residual_out, y, 
 def moe_rms_norm_backward(s: MoeShape, dy, dresidual, h, q_codes, q_scales, rstd, weight, token_mask, dx, dweight, ws,
                           stream=None) -> None:
     """dx and dweight from h, or (h None) from the MOE_Q_NORMALIZED checkpoint."""
-    import torch
     T, H = dy.shape[0], s.hidden
-    f32, b16 = torch.float32, torch.bfloat16
-    ct, st = _codes_types()
-    p = (_fit("dy", dy, (T, H), f32, b16), _fit("dresidual", dresidual, (T, H), f32, b16),
-         _fit("h", h, (T, H), f32, b16), _fit("q_codes", q_codes, (T, H), *ct),
-         _fit("q_scales", q_scales, (T, H // 32), *st), _fit("rstd", rstd, (T,), f32),
-         _fit("weight", weight, (H,), f32), _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool),
-         _fit("dx", dx, (T, H), f32, b16), _fit("dweight", dweight, (H,), f32))
+    p = (_fit("dy", dy, (T, H), _REAL), _fit("dresidual", dresidual, (T, H), _REAL),
+         _fit("h", h, (T, H), _REAL), _fit("q_codes", q_codes, (T, H), _CODES),
+         _fit("q_scales", q_scales, (T, H // 32), _SCALES), _fit("rstd", rstd, (T,), _F32),
+         _fit("weight", weight, (H,), _F32), _fit("token_mask", token_mask, (T,), _MASK),
+         _fit("dx", dx, (T, H), _REAL), _fit("dweight", dweight, (H,), _F32))
     _check(lib.moe_rms_norm_backward(ctypes.byref(s), T, _kind(dy), p[0], _kind(dresidual), p[1], _kind(h), p[2],
                                      p[3], p[4], p[5], p[6], p[7], _kind(dx), p[8], p[9], *_ws(ws),
                                      _stream(stream)))
@@ -361,27 +364,23 @@ def moe_balance_loss(s: MoeShape, logits, topk_ids, token_mask, seq_offsets, alp
                      prob_mean, ws, stream=None) -> None:
     """loss, counts [S][E], n_valid [S+1] and prob_mean [S][E] of S sequences
     (seq_offsets int32 [S+1]; None: one group of all tokens)."""
-    import torch
     T, E, S = logits.shape[0], s.n_experts, _n_seq(seq_offsets)
-    f32, i32 = torch.float32, torch.int32
-    p = (_fit("logits", logits, (T, E), f32), _fit("topk_ids", topk_ids, (T, s.top_k), i32),
-         _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool),
-         _fit("seq_offsets", seq_offsets, (S + 1,), i32), _fit("loss", loss, (1,), f32),
-         _fit("counts", counts, (S, E), i32), _fit("n_valid", n_valid, (S + 1,), i32),
-         _fit("prob_mean", prob_mean, (S, E), f32))
+    p = (_fit("logits", logits, (T, E), _F32), _fit("topk_ids", topk_ids, (T, s.top_k), _I32),
+         _fit("token_mask", token_mask, (T,), _MASK),
+         _fit("seq_offsets", seq_offsets, (S + 1,), _I32), _fit("loss", loss, (1,), _F32),
+         _fit("counts", counts, (S, E), _I32), _fit("n_valid", n_valid, (S + 1,), _I32),
+         _fit("prob_mean", prob_mean, (S, E), _F32))
     _check(lib.moe_balance_loss(ctypes.byref(s), T, p[0], p[1], p[2], p[3], S, alpha, p[4], p[5], p[6], p[7],
                                 *_ws(ws), _stream(stream)))
 
 
 def moe_balance_loss_backward(s: MoeShape, logits, token_mask, seq_offsets, alpha: float, dloss, counts, n_valid,
                               dlogits, stream=None) -> None:
-    import torch
     T, E, S = logits.shape[0], s.n_experts, _n_seq(seq_offsets)
-    f32, i32 = torch.float32, torch.int32
-    p = (_fit("logits", logits, (T, E), f32), _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool),
-         _fit("seq_offsets", seq_offsets, (S + 1,), i32), _fit("dloss", dloss, (1,), f32),
-         _fit("counts", counts, (S, E), i32), _fit("n_valid", n_valid, (S + 1,), i32),
-         _fit("dlogits", dlogits, (T, E), f32))
+    p = (_fit("logits", logits, (T, E), _F32), _fit("token_mask", token_mask, (T,), _MASK),
+         _fit("seq_offsets", seq_offsets, (S + 1,), _I32), _fit("dloss", dloss, (1,), _F32),
+         _fit("counts", counts, (S, E), _I32), _fit("n_valid", n_valid, (S + 1,), _I32),
+         _fit("dlogits", dlogits, (T, E), _F32))
     _check(lib.moe_balance_loss_backward(ctypes.byref(s), T, p[0], p[1], p[2], S, alpha, p[3], p[4], p[5], p[6],
                                          _stream(stream)))
 
@@ -391,21 +390,18 @@ def moe_route_backward(s: MoeShape, x, q_codes, q_scales, q_weight, w_router, re
     """dx, dw_router and dbias (each None if not wanted) from the gradient of
     the routing weights and / or dlogits_in; the layer's input as x (bfloat16)
     or as a checkpoint of moe_rms_norm."""
-    import torch
     H, E, k = s.hidden, s.n_experts, s.top_k
     g = dtopk_w if dtopk_w is not None else dlogits_in
     if g is None:
         raise ValueError("dtopk_w or dlogits_in must be given")
     T = g.shape[0]
-    f32, b16, i32 = torch.float32, torch.bfloat16, torch.int32
-    ct, st = _codes_types()
-    p = (_fit("x", x, (T, H), b16, torch.int16, torch.uint16), _fit("q_codes", q_codes, (T, H), *ct),
-         _fit("q_scales", q_scales, (T, H // 32), *st), _fit("q_weight", q_weight, (H,), f32),
-         _fit("w_router", w_router, (E, H), f32), _fit("logits", logits, (T, E), f32),
-         _fit("topk_ids", topk_ids, (T, k), i32), _fit("topk_w", topk_w, (T, k), f32),
-         _fit("dtopk_w", dtopk_w, (T, k), f32), _fit("dlogits_in", dlogits_in, (T, E), f32),
-         _fit("token_mask", token_mask, (T,), torch.uint8, torch.bool), _fit("dx", dx, (T, H), f32, b16),
-         _fit("dw_router", dw_router, (E, H), f32), _fit("dbias", dbias, (E,), f32))
+    p = (_fit("x", x, (T, H), _BITS16), _fit("q_codes", q_codes, (T, H), _CODES),
+         _fit("q_scales", q_scales, (T, H // 32), _SCALES), _fit("q_weight", q_weight, (H,), _F32),
+         _fit("w_router", w_router, (E, H), _F32), _fit("logits", logits, (T, E), _F32),
+         _fit("topk_ids", topk_ids, (T, k), _I32), _fit("topk_w", topk_w, (T, k), _F32),
+         _fit("dtopk_w", dtopk_w, (T, k), _F32), _fit("dlogits_in", dlogits_in, (T, E), _F32),
+         _fit("token_mask", token_mask, (T,), _MASK), _fit("dx", dx, (T, H), _REAL),
+         _fit("dw_router", dw_router, (E, H), _F32), _fit("dbias", dbias, (E,), _F32))
     _check(lib.moe_route_backward(ctypes.byref(s), T, p[0], p[1], p[2], p[3], p[4], int(bool(renormalize)), p[5],
                                   p[6], p[7], p[8], p[9], p[10], _kind(dx), p[11], p[12], p[13], *_ws(ws),
                                   _stream(stream)))

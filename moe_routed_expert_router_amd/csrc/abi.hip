@@ -56,7 +56,8 @@ moe_status check_tokens(int32_t T) {
 // A pointer the GPU will dereference: not NULL, aligned, known to the HIP
 // runtime as device memory or device-mapped host memory, and (where the runtime
 // reports the allocation's range) with `bytes` bytes inside that allocation.
-moe_status check_ptr(const void *p, size_t bytes, size_t align, const char *name) {
+// device, when given, receives the device of device memory, -1 for host memory.
+moe_status check_ptr(const void *p, size_t bytes, size_t align, const char *name, int *device = nullptr) {
     if (!p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
     if ((uintptr_t)p % align) return fail(MOE_ERR_MISALIGNED, "%s is not %zu-byte aligned", name, align);
     hipPointerAttribute_t at;
@@ -70,6 +71,7 @@ moe_status check_ptr(const void *p, size_t bytes, size_t align, const char *name
         return fail(MOE_ERR_NOT_DEVICE_ACCESSIBLE, "%s (%p) is unregistered host memory", name, p);
     if (at.type == hipMemoryTypeHost && at.devicePointer == nullptr)
         return fail(MOE_ERR_NOT_DEVICE_ACCESSIBLE, "%s (%p) is host memory not mapped for the device", name, p);
+    if (device) *device = at.type == hipMemoryTypeDevice ? at.device : -1;
     hipDeviceptr_t base = nullptr;
     size_t size = 0;
     e = hipMemGetAddressRange(&base, &size, const_cast<void *>(p));
@@ -295,20 +297,14 @@ private:
     }
     void add(const void *p, size_t bytes, size_t align, const char *name, bool out) {
         if (st_ != MOE_OK) return;
-        if ((st_ = check_ptr(p, bytes, align, name)) != MOE_OK) return;
-        if (dev_ < 0) {
+        int device = -1;
+        if ((st_ = check_ptr(p, bytes, align, name, &device)) != MOE_OK) return;
+        if (dev_ < 0)
             st_ = fail(MOE_ERR_HIP, "no usable current device");
-            return;
-        }
-        hipPointerAttribute_t at;
-        if (hipPointerGetAttributes(&at, p) != hipSuccess) {
-            (void)hipGetLastError();
-            st_ = fail(MOE_ERR_NOT_DEVICE_ACCESSIBLE, "%s (%p) is not memory known to HIP", name, p);
-        } else if (at.type == hipMemoryTypeDevice && at.device != dev_) {
-            st_ = fail(MOE_ERR_INVALID_ARG, "%s is memory of device %d, the current one is %d", name, at.device, dev_);
-        } else {
+        else if (device >= 0 && device != dev_)
+            st_ = fail(MOE_ERR_INVALID_ARG, "%s is memory of device %d, the current one is %d", name, device, dev_);
+        else
             b_[n_++] = {p, bytes, out, name};
-        }
     }
     int dev_ = -1, n_ = 0, n_pairs_ = 0;
     moe_status st_ = MOE_OK;

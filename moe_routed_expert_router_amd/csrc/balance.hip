@@ -16,11 +16,14 @@ namespace moe {
 
 namespace {
 
-constexpr int kBalWaves = 8;
+constexpr int kBalWaves = 16;
 constexpr int kBalThreads = 64 * kBalWaves;
 constexpr int kBalMaxChunks = 1024;
+// Tokens up to which one block does the whole loss of a single group (four
+// tokens per wave): one launch instead of two.
+constexpr int kBalOneTokens = 64;
 
-// Tokens per chunk: 32 (four per wave), more where that gave over 1024 chunks.
+// Tokens per chunk: 32 (two per wave), more where that gave over 1024 chunks.
 int chunk_tokens(int T) {
     const int n = (T + 32 * kBalMaxChunks - 1) / (32 * kBalMaxChunks);
     return 32 * (n > 1 ? n : 1);
@@ -108,57 +111,108 @@ struct BalanceWs {
     }
 };
 
-// Sums of one chunk: probabilities in registers over the wave's tokens, picks
-// in an LDS histogram (integers: the order of the additions is immaterial).
-template <int NPL>
-__global__ __launch_bounds__(kBalThreads) void balance_sums(BalanceArgs a, int R, BalanceWs w) {
-    __shared__ int hist[kMaxExperts];
+// Outputs of the loss.
+struct BalanceOut {
+    float *loss;
+    int32_t *counts, *n_valid;
+    float *prob_mean;
+};
+
+__device__ __forceinline__ float sum16(const float (&v)[kBalWaves]) {
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = (v[4 * i] + v[4 * i + 1]) + (v[4 * i + 2] + v[4 * i + 3]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Sums of one chunk: probabilities in registers over the wave's tokens (two at
+// a time, so that one's loads and reductions run beside the other's), picks in
+// an LDS histogram (integers: the order of the additions is immaterial).
+// ONE: the chunk is the whole batch and its only group; the block finishes the
+// loss itself.
+template <int NPL, bool ONE>
+__global__ __launch_bounds__(kBalThreads) void balance_sums(BalanceArgs a, int R, BalanceWs w, BalanceOut o) {
+    __shared__ int hist[64 * NPL];
     __shared__ float pl[kBalWaves][64 * NPL];
     __shared__ int ncount[kBalWaves];
+    __shared__ double dots[kBalWaves];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
     const int item = blockIdx.x;
-    if (item == 0 && tid == 0) *w.done = 0;   // read only by the next launch
-    const auto key = [&](int g) { return bound_of(a.offsets, g, a.T) / R + g; };
-    const int g = a.offsets ? last_group(a.S, item, key) : 0;
-    const int o0 = bound_of(a.offsets, g, a.T), o1 = bound_of(a.offsets, g + 1, a.T);
-    const int chunk = item - key(g);
-    const long long first = o0 + (long long)chunk * R;
-    // chunk < 0: an item before the first group's start
-    const int t0 = chunk >= 0 && first < o1 ? (int)first : o1, t1 = o1 - t0 > R ? t0 + R : o1;
-    for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
+    int t0 = 0, t1 = a.T;
+    if constexpr (!ONE) {
+        if (item == 0 && tid == 0) *w.done = 0;   // read only by the next launch
+        const auto key = [&](int g) { return bound_of(a.offsets, g, a.T) / R + g; };
+        const int g = a.offsets ? last_group(a.S, item, key) : 0;
+        const int o0 = bound_of(a.offsets, g, a.T), o1 = bound_of(a.offsets, g + 1, a.T);
+        const int chunk = item - key(g);
+        const long long first = o0 + (long long)chunk * R;
+        // chunk < 0: an item before the first group's start
+        t0 = chunk >= 0 && first < o1 ? (int)first : o1;
+        t1 = o1 - t0 > R ? t0 + R : o1;
+    }
+    if (tid < 64 * NPL) hist[tid] = 0;
     __syncthreads();
     float ps[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) ps[i] = 0.f;
     int n = 0;
-    for (int t = t0 + wave; t < t1; t += kBalWaves) {
-        if (a.mask && a.mask[t] == 0) continue;
-        float z[NPL], p[NPL];
-        load_row<NPL>(a.z + (size_t)t * E, E, z);
+    for (int t = t0 + wave; t < t1; t += 2 * kBalWaves) {
+        const int u = t + kBalWaves;
+        const bool in0 = !(a.mask && a.mask[t] == 0), in1 = u < t1 && !(a.mask && a.mask[u] == 0);
+        float z0[NPL], z1[NPL], p0[NPL], p1[NPL];
+        load_row<NPL>(a.z + (size_t)t * E, E, z0);
+        load_row<NPL>(a.z + (size_t)(u < t1 ? u : t) * E, E, z1);
         if (lane < a.k) {
-            const int id = a.ids[(size_t)t * a.k + lane];
-            if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+            const int i0 = in0 ? a.ids[(size_t)t * a.k + lane] : -1;
+            const int i1 = in1 ? a.ids[(size_t)u * a.k + lane] : -1;
+            if (i0 >= 0 && i0 < E) atomicAdd(&hist[i0], 1);
+            if (i1 >= 0 && i1 < E) atomicAdd(&hist[i1], 1);
         }
-        row_softmax<NPL>(z, p);
+        row_softmax<NPL>(z0, p0);
+        row_softmax<NPL>(z1, p1);
+        // a row that does not count is dropped by selection: it may hold NaN
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) ps[i] += p[i];
-        ++n;
+        for (int i = 0; i < NPL; ++i) ps[i] += (in0 ? p0[i] : 0.f) + (in1 ? p1[i] : 0.f);
+        n += (in0 ? 1 : 0) + (in1 ? 1 : 0);
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) pl[wave][lane + 64 * i] = ps[i];
     if (lane == 0) ncount[wave] = n;
     __syncthreads();
-    for (int e = tid; e < E; e += kBalThreads) {
-        float s[kBalWaves];
+    n = 0;
 #pragma unroll
-        for (int q = 0; q < kBalWaves; ++q) s[q] = pl[q][e];
-        w.psum[(size_t)item * E + e] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-        w.csum[(size_t)item * E + e] = hist[e];
+    for (int q = 0; q < kBalWaves; ++q) n += ncount[q];
+    double d = 0.0;
+    if (tid < E) {
+        float v[kBalWaves];
+#pragma unroll
+        for (int q = 0; q < kBalWaves; ++q) v[q] = pl[q][tid];
+        const float p = sum16(v);
+        const int c = hist[tid];
+        if constexpr (ONE) {
+            const float mean = n > 0 ? p / (float)n : 0.0f;
+            o.counts[tid] = c;
+            if (o.prob_mean) o.prob_mean[tid] = mean;
+            d = n > 0 ? (double)c / n * (double)mean : 0.0;
+        } else {
+            w.psum[(size_t)item * E + tid] = p;
+            w.csum[(size_t)item * E + tid] = c;
+        }
     }
-    if (tid == 0) {
-        int s = 0;
-        for (int q = 0; q < kBalWaves; ++q) s += ncount[q];
-        w.nsum[item] = s;
+    if constexpr (ONE) {
+        d = wave_sum_f64(d);
+        if (lane == 0) dots[wave] = d;
+        __syncthreads();
+        if (tid == 0) {
+            double s = 0.0;
+#pragma unroll
+            for (int q = 0; q < kBalWaves; ++q) s += dots[q];
+            o.n_valid[0] = n;
+            o.n_valid[1] = n > 0;
+            *o.loss = n > 0 ? (float)((double)a.alpha * E / a.k * s) : 0.0f;
+        }
+    } else if (tid == 0) {
+        w.nsum[item] = n;
     }
 }
 
@@ -171,10 +225,7 @@ __device__ __forceinline__ int group_tokens(const BalanceWs &w, int i0, int i1) 
 
 // Block (column tile, group): adds the group's chunks, 64 experts each; the
 // block that finishes last adds the groups' parts of the loss in their order.
-__global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int R, BalanceWs w,
-                                                              float *__restrict__ loss, int32_t *__restrict__ counts,
-                                                              int32_t *__restrict__ n_valid,
-                                                              float *__restrict__ prob_mean) {
+__global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int R, BalanceWs w, BalanceOut o) {
     __shared__ float ps[kBalWaves][64];
     __shared__ int cs[kBalWaves][64];
     __shared__ int last;
@@ -186,11 +237,13 @@ __global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int
     const int n = group_tokens(w, i0, i1);
     float p = 0.f;
     int c = 0;
-    if (e < E)
+    if (e < E) {
+#pragma unroll 8
         for (int i = i0 + wave; i < i1; i += kBalWaves) {
             p += w.psum[(size_t)i * E + e];
             c += w.csum[(size_t)i * E + e];
         }
+    }
     ps[wave][lane] = p;
     cs[wave][lane] = c;
     __syncthreads();
@@ -202,16 +255,16 @@ __global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int
             v[q] = ps[q][lane];
             c += cs[q][lane];
         }
-        p = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        p = sum16(v);
         const float mean = n > 0 ? p / (float)n : 0.0f;
         if (e < E) {
-            counts[(size_t)g * E + e] = c;
-            if (prob_mean) prob_mean[(size_t)g * E + e] = mean;
+            o.counts[(size_t)g * E + e] = c;
+            if (o.prob_mean) o.prob_mean[(size_t)g * E + e] = mean;
         }
         const double d = wave_sum_f64(e < E && n > 0 ? (double)c / n * (double)mean : 0.0);
         if (lane == 0) {
             w.dot[(size_t)g * ntile + blockIdx.x] = d;
-            if (blockIdx.x == 0) n_valid[g] = n;
+            if (blockIdx.x == 0) o.n_valid[g] = n;
             __threadfence();   // the part is visible before the count says so
             last = atomicAdd(w.done, 1u) == gridDim.x * gridDim.y - 1;
         }
@@ -223,12 +276,12 @@ __global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int
         double s = 0.0;
         int live = 0;
         for (int q = lane; q < a.S * ntile; q += 64) s += w.dot[q];
-        for (int q = lane; q < a.S; q += 64) live += n_valid[q] > 0;
+        for (int q = lane; q < a.S; q += 64) live += o.n_valid[q] > 0;
         s = wave_sum_f64(s);
         live = wave_sum_int(live);
         if (lane == 0) {
-            n_valid[a.S] = live;
-            *loss = live > 0 ? (float)((double)a.alpha * E / a.k * s / live) : 0.0f;
+            o.n_valid[a.S] = live;
+            *o.loss = live > 0 ? (float)((double)a.alpha * E / a.k * s / live) : 0.0f;
         }
     }
 }
@@ -290,34 +343,32 @@ size_t balance_ws_bytes(int T, int E, int S) {
     return BalanceWs::layout(chunk_items(T, S), E, S, nullptr, nullptr);
 }
 
-#define MOE_BY_NPL(E, CALL)       \
-    switch (topk_npl(E)) {        \
-        case 1: CALL(1); break;   \
-        case 2: CALL(2); break;   \
-        case 4: CALL(4); break;   \
-        case 8: CALL(8); break;   \
-        default: CALL(16); break; \
-    }
-
 hipError_t launch_balance_loss(const BalanceArgs &a, float *loss, int32_t *counts, int32_t *n_valid, float *prob_mean,
                                char *ws, hipStream_t st) {
+    const BalanceOut o{loss, counts, n_valid, prob_mean};
     const int R = chunk_tokens(a.T), items = chunk_items(a.T, a.S);
     BalanceWs w;
     BalanceWs::layout(items, a.E, a.S, ws, &w);
-#define CALL(N) MOE_LAUNCH("balance_sums", balance_sums<N>, dim3(items), dim3(kBalThreads), 0, st, a, R, w)
+    if (a.offsets == nullptr && a.T <= kBalOneTokens) {
+#define CALL(N) MOE_LAUNCH("balance_sums", (balance_sums<N, true>), dim3(1), dim3(kBalThreads), 0, st, a, R, w, o)
+        MOE_BY_NPL(a.E, CALL)
+#undef CALL
+        return hipGetLastError();
+    }
+#define CALL(N) MOE_LAUNCH("balance_sums", (balance_sums<N, false>), dim3(items), dim3(kBalThreads), 0, st, a, R, w, o)
     MOE_BY_NPL(a.E, CALL)
 #undef CALL
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    MOE_LAUNCH("balance_reduce", balance_reduce, dim3((a.E + 63) / 64, a.S), dim3(kBalThreads), 0, st, a, R, w, loss,
-               counts, n_valid, prob_mean);
+    MOE_LAUNCH("balance_reduce", balance_reduce, dim3((a.E + 63) / 64, a.S), dim3(kBalThreads), 0, st, a, R, w, o);
     return hipGetLastError();
 }
 
 hipError_t launch_balance_loss_backward(const BalanceArgs &a, const float *dloss, const int32_t *counts,
                                         const int32_t *n_valid, float *dz, hipStream_t st) {
     if (a.T == 0) return hipSuccess;
-    const int rows = a.T <= 4096 ? 4 : 16;
+    // a token per wave until the chip is full several times over, then four
+    const int rows = a.T <= 32768 ? 4 : 16;
     const dim3 g((a.T + rows - 1) / rows);
 #define CALL(N) MOE_LAUNCH("balance_backward", balance_backward<N>, g, dim3(256), 0, st, a, rows, dloss, counts, n_valid, dz)
     MOE_BY_NPL(a.E, CALL)

@@ -110,6 +110,73 @@ __device__ __forceinline__ void split8(const float *v, uint4 *o) {
 }
 
 // --------------------------------- dz --------------------------------------
+// dz of token t's row: v[i] for expert lane + 64 i (0 past E, for a masked
+// token and for t >= T).
+template <int NPL>
+__device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[NPL]) {
+    const int lane = threadIdx.x & 63, E = a.E, k = a.k;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = 0.f;
+    if (t >= a.T || (a.mask && a.mask[t] == 0)) return;
+    const size_t at = (size_t)t * E;
+    if (a.dz_in) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (lane + 64 * i < E) v[i] = a.dz_in[at + lane + 64 * i];
+    }
+    if (a.dw) {
+        int id = -1;
+        float w = 0.f, d = 0.f;
+        if (lane < k) {
+            id = a.ids[(size_t)t * k + lane];
+            w = a.w[(size_t)t * k + lane];
+            d = a.dw[(size_t)t * k + lane];
+        }
+        if (id < 0 || id >= E) id = -1;
+        // a pick outside [0, E) added nothing to the output: its weight has no gradient
+        const float dot = wave_sum(id >= 0 ? w * d : 0.f);
+        if (a.renorm) {
+            const float u = w * ((id >= 0 ? d : 0.f) - dot);
+            for (int j = 0; j < k; ++j) {
+                const int ej = __builtin_amdgcn_readlane(id, j);
+                const float uj = readlanef(u, j);
+#pragma unroll
+                for (int i = 0; i < NPL; ++i)
+                    if (lane + 64 * i == ej) v[i] += uj;
+            }
+        } else {
+            float z[NPL], m = -INFINITY, s = 0.f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int e = lane + 64 * i;
+                z[i] = e < E ? a.z[at + e] : -INFINITY;
+                z[i] = z[i] == z[i] ? z[i] : -INFINITY;   // as the forward: NaN is left out of the sum
+                m = fmaxf(m, z[i]);
+            }
+            m = wave_max(m);
+            m = m == -INFINITY ? 0.f : m;
+            float g[NPL];
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                z[i] = expf(z[i] - m);
+                s += z[i];
+                g[i] = -dot;
+            }
+            s = wave_sum(s);
+            const float inv = s == 0.f ? 0.f : 1.f / s;
+            for (int j = 0; j < k; ++j) {
+                const int ej = __builtin_amdgcn_readlane(id, j);
+                const float dj = readlanef(d, j);
+#pragma unroll
+                for (int i = 0; i < NPL; ++i)
+                    if (lane + 64 * i == ej) g[i] += dj;
+            }
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) v[i] = fmaf(z[i] * inv, g[i], v[i]);
+        }
+    }
+}
+
 // 32 tokens per block, one wave per token at a time: dz of the row in
 // registers, then in an LDS tile from which it leaves in both operand orders
 // (token rows for dx, expert rows for dWr) and as the block's part of db.
@@ -119,72 +186,11 @@ __global__ __launch_bounds__(512) void route_dz(RouteBwdArgs a, uint8_t *__restr
                                                 float *__restrict__ dbp, int EC, int EG) {
     constexpr int kPitch = 64 * NPL + 4;
     __shared__ __align__(16) float tile[kDzTok][kPitch];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E, k = a.k;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
     const int tgrp = blockIdx.x, tok0 = tgrp * kDzTok;
     for (int r = wave; r < kDzTok; r += 8) {
-        const int t = tok0 + r;
         float v[NPL];
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) v[i] = 0.f;
-        if (t < a.T && !(a.mask && a.mask[t] == 0)) {
-            const size_t at = (size_t)t * E;
-            if (a.dz_in) {
-#pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (lane + 64 * i < E) v[i] = a.dz_in[at + lane + 64 * i];
-            }
-            if (a.dw) {
-                int id = -1;
-                float w = 0.f, d = 0.f;
-                if (lane < k) {
-                    id = a.ids[(size_t)t * k + lane];
-                    w = a.w[(size_t)t * k + lane];
-                    d = a.dw[(size_t)t * k + lane];
-                }
-                if (id < 0 || id >= E) id = -1;
-                // a pick outside [0, E) added nothing to the output: its weight has no gradient
-                const float dot = wave_sum(id >= 0 ? w * d : 0.f);
-                if (a.renorm) {
-                    const float u = w * ((id >= 0 ? d : 0.f) - dot);
-                    for (int j = 0; j < k; ++j) {
-                        const int ej = __builtin_amdgcn_readlane(id, j);
-                        const float uj = readlanef(u, j);
-#pragma unroll
-                        for (int i = 0; i < NPL; ++i)
-                            if (lane + 64 * i == ej) v[i] += uj;
-                    }
-                } else {
-                    float z[NPL], m = -INFINITY, s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i) {
-                        const int e = lane + 64 * i;
-                        z[i] = e < E ? a.z[at + e] : -INFINITY;
-                        z[i] = z[i] == z[i] ? z[i] : -INFINITY;   // as the forward: NaN is left out of the sum
-                        m = fmaxf(m, z[i]);
-                    }
-                    m = wave_max(m);
-                    m = m == -INFINITY ? 0.f : m;
-                    float g[NPL];
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i) {
-                        z[i] = expf(z[i] - m);
-                        s += z[i];
-                        g[i] = -dot;
-                    }
-                    s = wave_sum(s);
-                    const float inv = s == 0.f ? 0.f : 1.f / s;
-                    for (int j = 0; j < k; ++j) {
-                        const int ej = __builtin_amdgcn_readlane(id, j);
-                        const float dj = readlanef(d, j);
-#pragma unroll
-                        for (int i = 0; i < NPL; ++i)
-                            if (lane + 64 * i == ej) g[i] += dj;
-                    }
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i) v[i] = fmaf(z[i] * inv, g[i], v[i]);
-                }
-            }
-        }
+        dz_row<NPL>(a, tok0 + r, v);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) tile[r][lane + 64 * i] = v[i];
     }
@@ -544,6 +550,184 @@ __global__ __launch_bounds__(256) void route_zero(float *p, size_t n) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0.f;
 }
 
+// ------------------------------ few tokens ---------------------------------
+// Up to kFewTokens the operands' splits and re-layouts cost more than the
+// products: dz as fp32 rows [T][E8] (E rounded up to 8, zeros past E), and
+// both products straight from the fp32 operands on the 32x32x2 fp32 MFMA, in
+// one launch whose blocks have one of three roles (dx, dWr, db).
+constexpr int kFewTokens = 32;
+
+template <int NPL>
+__global__ __launch_bounds__(256) void route_dz_rows(RouteBwdArgs a, float *__restrict__ dz, int E8) {
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (t >= a.T) return;
+    float v[NPL];
+    dz_row<NPL>(a, t, v);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        if (lane + 64 * i < E8) dz[(size_t)t * E8 + lane + 64 * i] = v[i];
+}
+
+// D += A B, lane l: A[l % 32][l / 32], B[l / 32][l % 32]; D as in mfma32x32x16.
+__device__ __forceinline__ f32x16 mfma32x32x2(float a, float b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+
+// dx of 32 tokens x 32 hidden columns: eight waves share the experts in
+// pieces of 8 (lane half h takes experts 4 h .. +3 of a piece, one per MFMA),
+// then add their tiles in wave order through LDS.
+template <typename DX>
+__device__ void few_dx(const RouteBwdArgs &a, const float *__restrict__ dz, int E8, int block, float *lds) {
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, half = lane >> 5;
+    const int HG = a.H / 32, hg = block % HG, tg = block / HG;
+    const int h = 32 * hg + (lane & 31), t = 32 * tg + (lane & 31);
+    const int np = E8 / 8, per = (np + 7) / 8;
+    const int p0 = wave * per, p1 = p0 + per < np ? p0 + per : np;
+    const float *drow = dz + (size_t)(t < a.T ? t : 0) * E8 + 4 * half;
+    f32x16 acc;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    constexpr int kAt = 3;   // pieces whose loads are all in flight before the first use
+    for (int q = p0; q < p1; q += kAt) {
+        float4 d[kAt];
+        float w[kAt][4];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+            const int p = q + j < p1 ? q + j : p1 - 1;
+            d[j] = *reinterpret_cast<const float4 *>(drow + 8 * p);
+            if (t >= a.T || q + j >= p1) d[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = 8 * p + 4 * half + i;   // past E the row of dz is zero: any finite weight does
+                w[j][i] = a.wr[(size_t)(e < a.E ? e : a.E - 1) * a.H + h];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+            acc = mfma32x32x2(d[j].x, w[j][0], acc);
+            acc = mfma32x32x2(d[j].y, w[j][1], acc);
+            acc = mfma32x32x2(d[j].z, w[j][2], acc);
+            acc = mfma32x32x2(d[j].w, w[j][3], acc);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) lds[(wave * 16 + i) * 64 + lane] = acc[i];
+    __syncthreads();
+    // thread: token tid / 16 of the group, columns 2 (tid % 16), + 1
+    const int tt = tid >> 4, c = 2 * (tid & 15);
+    if (32 * tg + tt >= a.T) return;
+    const int at = ((tt & 3) + 4 * (tt >> 3)) * 64 + 32 * ((tt >> 2) & 1) + c;
+    float2 s = *reinterpret_cast<const float2 *>(lds + at);
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+        const float2 v = *reinterpret_cast<const float2 *>(lds + w * 1024 + at);
+        s.x += v.x;
+        s.y += v.y;
+    }
+    const size_t o = (size_t)(32 * tg + tt) * a.H + 32 * hg + c;
+    if constexpr (__is_same(DX, float))
+        *reinterpret_cast<float2 *>(static_cast<float *>(a.dx) + o) = s;
+    else
+        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.dx) + o) = bf16x2_bits(s.x, s.y);
+}
+
+// dWr of 32 experts x 64 hidden columns per wave: the contraction over the
+// tokens, two per MFMA.  A lane loads the columns 2 c and 2 c + 1 of a token
+// at once; the even ones make one tile, the odd ones another.
+template <bool MX>
+__device__ void few_dwr(const RouteBwdArgs &a, const float *__restrict__ dz, int E8, int block) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+    const int HB = (a.H + 511) / 512, hb = block % HB, eg = block / HB;
+    const int h = 512 * hb + 64 * wave + 2 * (lane & 31);
+    if (512 * hb + 64 * wave >= a.H) return;
+    const int e = 32 * eg + (lane & 31), ec = e < E8 ? e : E8 - 1;   // past E8: not stored
+    f32x16 acc[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+    for (int t0 = 0; t0 < a.T; t0 += 16) {
+        float d[8], x0[8], x1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + 2 * i + half;
+            const bool in = t < a.T && !(a.mask && a.mask[t] == 0);
+            const int tc = in ? t : 0;
+            d[i] = in ? dz[(size_t)tc * E8 + ec] : 0.f;
+            const size_t at = (size_t)tc * a.H + h;
+            if constexpr (MX) {
+                typedef float f2 __attribute__((ext_vector_type(2)));
+                const uint32_t v = *reinterpret_cast<const uint16_t *>(a.codes + at);
+                const float sc = e8m0_to_f32(a.scales[at >> 5]);
+                const f2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)v, false);
+                x0[i] = in ? f[0] * sc : 0.f;
+                x1[i] = in ? f[1] * sc : 0.f;
+            } else {
+                const uint32_t v = *reinterpret_cast<const uint32_t *>(a.x + at);
+                x0[i] = in ? __uint_as_float(v << 16) : 0.f;
+                x1[i] = in ? __uint_as_float(v & 0xffff0000u) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            acc[0] = mfma32x32x2(d[i], x0[i], acc[0]);
+            acc[1] = mfma32x32x2(d[i], x1[i], acc[1]);
+        }
+    }
+    float w0 = 1.f, w1 = 1.f;
+    if (MX && a.q_weight) {
+        w0 = a.q_weight[h];
+        w1 = a.q_weight[h + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int er = 32 * eg + 8 * (i / 4) + 4 * half + i % 4;
+        if (er < a.E)
+            *reinterpret_cast<float2 *>(a.dwr + (size_t)er * a.H + h) = make_float2(acc[0][i] * w0, acc[1][i] * w1);
+    }
+}
+
+template <bool MX, typename DX>
+__global__ __launch_bounds__(512) void route_few(RouteBwdArgs a, const float *__restrict__ dz, int E8, int n_dx,
+                                                 int n_dwr) {
+    __shared__ __align__(16) float lds[8 * 16 * 64];
+    const int b = blockIdx.x;
+    if (b < n_dx) {
+        few_dx<DX>(a, dz, E8, b, lds);
+    } else if (b < n_dx + n_dwr) {
+        few_dwr<MX>(a, dz, E8, b - n_dx);
+    } else {
+        const int e = (b - n_dx - n_dwr) * 512 + threadIdx.x;
+        if (e < a.E) {
+            float s = 0.f;
+            for (int t = 0; t < a.T; ++t) s += dz[(size_t)t * E8 + e];
+            a.db[e] = s;
+        }
+    }
+}
+
+hipError_t launch_few(const RouteBwdArgs &a, char *ws, hipStream_t st) {
+    float *dz = reinterpret_cast<float *>(ws);
+    const int E8 = (a.E + 7) & ~7;
+#define MOE_DZ(N) MOE_LAUNCH("route_dz_rows", route_dz_rows<N>, dim3((a.T + 3) / 4), dim3(256), 0, st, a, dz, E8)
+    MOE_BY_NPL(a.E, MOE_DZ)
+#undef MOE_DZ
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int n_dx = a.dx ? (a.T + 31) / 32 * (a.H / 32) : 0;
+    const int n_dwr = a.dwr ? (a.E + 31) / 32 * ((a.H + 511) / 512) : 0;
+    const int n_db = a.db ? (a.E + 511) / 512 : 0;
+    const dim3 g(n_dx + n_dwr + n_db), b(512);
+    const bool mx = a.x == nullptr, f = a.dx_dtype == MOE_OUT_F32;
+    if (mx && f)
+        MOE_LAUNCH("route_few", (route_few<true, float>), g, b, 0, st, a, dz, E8, n_dx, n_dwr);
+    else if (mx)
+        MOE_LAUNCH("route_few", (route_few<true, Bf16>), g, b, 0, st, a, dz, E8, n_dx, n_dwr);
+    else if (f)
+        MOE_LAUNCH("route_few", (route_few<false, float>), g, b, 0, st, a, dz, E8, n_dx, n_dwr);
+    else
+        MOE_LAUNCH("route_few", (route_few<false, Bf16>), g, b, 0, st, a, dz, E8, n_dx, n_dwr);
+    return hipGetLastError();
+}
+
 template <int NP>
 void launch_dz(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
     uint8_t *dza = a.dx ? reinterpret_cast<uint8_t *>(ws + w.dza) : nullptr;
@@ -551,13 +735,7 @@ void launch_dz(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st
     float *dbp = a.db ? reinterpret_cast<float *>(ws + w.dbp) : nullptr;
     const dim3 g(w.tg), b(512);
 #define MOE_DZ(N) MOE_LAUNCH("route_dz", (route_dz<N, NP>), g, b, 0, st, a, dza, dzt, dbp, w.ec, w.eg)
-    switch (topk_npl(a.E)) {
-        case 1: MOE_DZ(1); break;
-        case 2: MOE_DZ(2); break;
-        case 4: MOE_DZ(4); break;
-        case 8: MOE_DZ(8); break;
-        default: MOE_DZ(16); break;
-    }
+    MOE_BY_NPL(a.E, MOE_DZ)
 #undef MOE_DZ
 }
 
@@ -572,7 +750,10 @@ void launch_dx(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st
 
 }  // namespace
 
-size_t route_bwd_ws_bytes(int T, int H, int E) { return route_ws(T, H, E, 3).total; }
+size_t route_bwd_ws_bytes(int T, int H, int E) {
+    if (T <= kFewTokens) return WsLayout::up((size_t)T * ((E + 7) & ~7) * 4);
+    return route_ws(T, H, E, 3).total;
+}
 
 hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st) {
     const int planes = a.dx_dtype == MOE_OUT_F32 ? 3 : 2;
@@ -583,6 +764,7 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st
         if (a.db) MOE_LAUNCH("route_zero", route_zero, dim3(1), dim3(256), 0, st, a.db, (size_t)a.E);
         return hipGetLastError();
     }
+    if (a.T <= kFewTokens) return launch_few(a, ws, st);
     if (planes == 3)
         launch_dz<3>(a, w, ws, st);
     else

@@ -75,6 +75,20 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st
 // (fixed for a given R); part [R][C].  R = 0 writes zeros.
 hipError_t launch_column_sum(const char *name, const float *part, int R, int C, float *out, hipStream_t st);
 
+// CALL(N) with N >= ceil(E / 64) logits per lane of a wave.
+#define MOE_BY_NPL(E, CALL)             \
+    switch (((E) + 63) / 64) {          \
+        case 1: CALL(1); break;         \
+        case 2: CALL(2); break;         \
+        case 3:                         \
+        case 4: CALL(4); break;         \
+        case 5:                         \
+        case 6: CALL(6); break;         \
+        case 7:                         \
+        case 8: CALL(8); break;         \
+        default: CALL(16); break;       \
+    }
+
 // ------------------------------ device code --------------------------------
 struct Bf16 {};   // tag: 16-bit storage
 struct Mx8 {};    // tag: e4m3 codes with an e8m0 scale per 32

@@ -640,7 +640,8 @@ def test_refusals():
     ws = new_ws(s, T, 3)
     refuse(moe.MOE_ERR_WORKSPACE_TOO_SMALL, moe.moe_rms_norm_backward, s, dy, None, c.x, None, None, r, c.w, None, None,
            dw, ws[:256])
-    refuse(bad, moe.moe_rms_norm_backward, s, dy, None, c.x, None, None, r, c.w, None, None, dw, new_ws(s, T, 9)[16:])
+    refuse(bad, moe.moe_rms_norm_backward, s, dy, None, c.x, None, None, r, c.w, None, None, dw,
+           torch.empty(moe.moe_train_workspace_bytes(s, T) + 256, dtype=torch.uint8, device="cuda")[16:])
     refuse(arg, moe.moe_rms_norm_backward, s, dy, None, c.x, c.c, c.sc, r, c.w, None, None, dw, ws)   # two sources
     refuse(arg, moe.moe_rms_norm_backward, s, dy, None, None, None, None, r, c.w, None, None, dw, ws)  # none
     refuse(arg, moe.moe_rms_norm_backward, s, dy, None, c.x, None, None, r, c.w, None, None, None, ws)
