@@ -33,21 +33,22 @@ constexpr int kDzTok = 32;    // tokens per block of route_dz
 // ------------------------------- workspace ---------------------------------
 struct RouteWs {
     int tg, ec, eg, hg;   // groups: 32 tokens, 16 experts (even), 32 experts, 32 hidden columns
-    size_t dza, dzt, wrp, dbp, dwp, total;
+    size_t dza, dzt, wrp, valid, dbp, dwp, total;
     int splits;
 };
 
-constexpr int kTileE = 128, kTileH = 128, kTileT = 128;
+constexpr int kTileE = 128, kTileH = 256, kTileT = 128;
 constexpr int kStepK = 32;
 constexpr int kMaxSplits = 16;
+constexpr int kCus = 256;   // compute units: one block of the product kernels on each
 
-// Token splits of the dWr product: as many as bring the (expert, hidden)
-// tiles to about 512 blocks (two per CU), each with at least 8 steps of 32
-// tokens, at most kMaxSplits (every split writes and re-reads a partial dWr).
+// Token splits of the dWr product: as many as keep its (expert, hidden) tiles
+// within one round of blocks, each with at least 4 steps of 32 tokens, at most
+// kMaxSplits (every split writes and re-reads a partial dWr).
 int dw_splits(int T, int H, int E) {
     const int tiles = ((E + kTileE - 1) / kTileE) * ((H + kTileH - 1) / kTileH);
-    int s = 512 / tiles;
-    const int most = (T + 8 * kStepK - 1) / (8 * kStepK);
+    int s = kCus / tiles;
+    const int most = (T + 4 * kStepK - 1) / (4 * kStepK);
     s = s < most ? s : most;
     return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
 }
@@ -68,6 +69,7 @@ RouteWs route_ws(int T, int H, int E, int planes) {
     w.dza = take((size_t)w.tg * w.ec * planes * kUnit);
     w.dzt = take((size_t)w.tg * 2 * w.eg * 3 * kUnit);
     w.wrp = take((size_t)w.hg * w.ec * planes * kUnit);
+    w.valid = take((size_t)w.tg * 4);
     w.dbp = take((size_t)w.tg * E * 4);
     w.dwp = take((size_t)w.splits * E * H * 4);
     w.total = at;
@@ -177,36 +179,82 @@ __device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[
     }
 }
 
-// 32 tokens per block, one wave per token at a time: dz of the row in
-// registers, then in an LDS tile from which it leaves in both operand orders
-// (token rows for dx, expert rows for dWr) and as the block's part of db.
-// Tokens past T and masked tokens have dz = 0.
-template <int NPL, int NP>
-__global__ __launch_bounds__(512) void route_dz(RouteBwdArgs a, uint8_t *__restrict__ dza, uint8_t *__restrict__ dzt,
-                                                float *__restrict__ dbp, int EC, int EG) {
-    constexpr int kPitch = 64 * NPL + 4;
-    __shared__ __align__(16) float tile[kDzTok][kPitch];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
-    const int tgrp = blockIdx.x, tok0 = tgrp * kDzTok;
-    for (int r = wave; r < kDzTok; r += 8) {
-        float v[NPL];
-        dz_row<NPL>(a, tok0 + r, v);
+// Wr [E][H] as units (32 hidden columns, 16 experts): 256 columns of one
+// 32-expert group, through an LDS tile; each of the 16 waves leaves one unit.
+constexpr int kWrPitch = 257;
+template <int NP>
+__device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int EC, int block, float *tile) {
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int HB = (a.H + 255) / 256, h0 = 256 * (block % HB), eg = block / HB;
+    {
+        const int c = tid & 255, h = h0 + c < a.H ? h0 + c : a.H - 1;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) tile[r][lane + 64 * i] = v[i];
+        for (int r = 0; r < 8; ++r) {
+            const int e = 32 * eg + (tid >> 8) + 4 * r;
+            v[r] = e < a.E ? a.wr[(size_t)e * a.H + h] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) tile[((tid >> 8) + 4 * r) * kWrPitch + c] = v[r];
     }
     __syncthreads();
-    if (dbp) {
-        for (int e = tid; e < E; e += 512) {
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const int hg = wave >> 1, ch = wave & 1;
+    if (h0 + 32 * hg >= a.H) return;
+    float v[8];
 #pragma unroll
-            for (int r = 0; r < kDzTok; ++r) s[r & 3] += tile[r][e];
-            dbp[(size_t)tgrp * E + e] = (s[0] + s[1]) + (s[2] + s[3]);
-        }
+    for (int i = 0; i < 8; ++i) v[i] = tile[(16 * ch + 8 * (lane >> 5) + i) * kWrPitch + 32 * hg + (lane & 31)];
+    uint4 o[NP];
+    split8<NP>(v, o);
+    const size_t unit = (size_t)(h0 / 32 + hg) * EC + 2 * eg + ch;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint4 *>(out + (unit * NP + q) * kUnit + 16 * lane) = o[q];
+}
+
+// The operands of both products.  Blocks [0, tg): 32 tokens each, a wave per
+// token at a time: dz of the row in registers, then in an LDS tile from which
+// it leaves in both operand orders (token rows for dx, expert rows for dWr)
+// and as the block's part of db; tokens past T and masked tokens have dz = 0.
+// Blocks past tg (for dx): the router weight.
+template <int NPL, int NP>
+__global__ __launch_bounds__(1024) void route_operands(RouteBwdArgs a, uint8_t *__restrict__ dza,
+                                                       uint8_t *__restrict__ dzt, uint8_t *__restrict__ wrp,
+                                                       uint32_t *__restrict__ valid, float *__restrict__ dbp, int TG,
+                                                       int EC, int EG) {
+    constexpr int kPitch = 64 * NPL + 4;
+    constexpr int kDzLds = kDzTok * kPitch, kWrLds = 32 * kWrPitch;
+    __shared__ __align__(16) float lds[kDzLds > kWrLds ? kDzLds : kWrLds];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
+    const int tgrp = blockIdx.x, tok0 = tgrp * kDzTok;
+    if (tgrp >= TG) {
+        wr_units<NP>(a, wrp, EC, tgrp - TG, lds);
+        return;
+    }
+    float(*tile)[kPitch] = reinterpret_cast<float(*)[kPitch]>(lds);
+    {
+        float v[2][NPL];
+        dz_row<NPL>(a, tok0 + wave, v[0]);
+        dz_row<NPL>(a, tok0 + wave + 16, v[1]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) tile[wave + 16 * r][lane + 64 * i] = v[r][i];
+    }
+    if (wave == 0) {   // a bit per token of the group that counts
+        const int t = tok0 + lane;
+        const uint64_t in = __ballot(lane < 32 && t < a.T && !(a.mask && a.mask[t < a.T ? t : 0] == 0));
+        if (lane == 0) valid[tgrp] = (uint32_t)in;
+    }
+    __syncthreads();
+    if (dbp && tid < E) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < kDzTok; ++r) s[r & 3] += tile[r][tid];
+        dbp[(size_t)tgrp * E + tid] = (s[0] + s[1]) + (s[2] + s[3]);
     }
     // token rows: the 16-expert chunk ec of this token group, lane (token
     // l % 32, experts 8 (l / 32) .. +7); columns E .. 16 EC - 1 of the tile are 0
     if (dza) {
-        for (int ec = wave; ec < EC; ec += 8) {
+        for (int ec = wave; ec < EC; ec += 16) {
             const float *p = &tile[lane & 31][16 * ec + 8 * (lane >> 5)];
             float v[8];
 #pragma unroll
@@ -221,7 +269,7 @@ __global__ __launch_bounds__(512) void route_dz(RouteBwdArgs a, uint8_t *__restr
     // expert rows: units (16-token chunk, 32 experts), lane (expert l % 32,
     // tokens 8 (l / 32) .. +7)
     if (dzt) {
-        for (int u = wave; u < 2 * EG; u += 8) {
+        for (int u = wave; u < 2 * EG; u += 16) {
             const int half = u / EG, eg = u - half * EG;
             float v[8];
 #pragma unroll
@@ -236,32 +284,6 @@ __global__ __launch_bounds__(512) void route_dz(RouteBwdArgs a, uint8_t *__restr
     }
 }
 
-// ----------------------------- router weight -------------------------------
-// Wr [E][H] as units (32 hidden columns, 16 experts): block = 64 columns of
-// one 32-expert group, through an LDS tile.
-template <int NP>
-__global__ __launch_bounds__(256) void route_wr_units(const float *__restrict__ wr, int E, int H,
-                                                      uint8_t *__restrict__ out, int EC) {
-    __shared__ float tile[32][65];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int h0 = blockIdx.x * 64, e0 = blockIdx.y * 32;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const int e = e0 + wave * 8 + r;
-        tile[wave * 8 + r][lane] = e < E ? wr[(size_t)e * H + h0 + lane] : 0.f;
-    }
-    __syncthreads();
-    const int hg = wave >> 1, ch = wave & 1;   // a wave: one unit
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = tile[16 * ch + 8 * (lane >> 5) + i][32 * hg + (lane & 31)];
-    uint4 o[NP];
-    split8<NP>(v, o);
-    const size_t unit = (size_t)(2 * blockIdx.x + hg) * EC + 2 * blockIdx.y + ch;
-#pragma unroll
-    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint4 *>(out + (unit * NP + q) * kUnit + 16 * lane) = o[q];
-}
-
 // ----------------------------------- dx ------------------------------------
 __device__ __forceinline__ bf16x8 lds_unit(const uint8_t *p) {
     return *reinterpret_cast<const bf16x8 *>(p + 16 * (threadIdx.x & 63));
@@ -272,41 +294,114 @@ __device__ __forceinline__ void fill_unit(const uint8_t *src, uint8_t *dst) {
     lds_fill<16>(buffer_rsrc(src, kUnit), 16 * (threadIdx.x & 63), dst);
 }
 
-// dx tile: 128 tokens x 128 hidden columns, contraction over the experts in
-// steps of 32; four waves of 64 x 64.  MFMA rows = hidden columns, columns =
-// tokens: a lane ends with four consecutive columns of one token.
+// Tiles of dx in the order an XCD takes them: hidden tiles in groups of `hper`
+// (an eighth of them), token tiles outside, so that the blocks of one XCD share
+// few rows of Wr and all of them reuse the dz rows they bring into its L2.
+struct DxTiles {
+    int HT, TT, hper;
+    __device__ __forceinline__ void at(int idx, int &ht, int &tt) const {
+        const int grp = idx / (TT * hper), in = idx - grp * TT * hper;
+        const int width = HT - grp * hper < hper ? HT - grp * hper : hper;
+        tt = in / width;
+        ht = grp * hper + in - tt * width;
+    }
+};
+
+// dx = dz Wr: 128 tokens x 256 hidden columns per tile, contraction over the
+// experts in steps of 32, eight waves of 64 x 64.  MFMA rows = hidden columns,
+// columns = tokens: a lane ends with four consecutive columns of one token.
+// One block per compute unit takes every 32nd tile of its XCD's share and runs
+// their steps as one sequence, so that the next tile's operands are on their
+// way while a tile is finished and stored.  LDS is a ring of RS stages (three
+// for two terms, two for three, 144 KB), filled RS - 1 steps ahead.
 template <int NP, typename DX>
-__global__ __launch_bounds__(256) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp, int T,
-                                                int H, int EC, int TG, void *__restrict__ dx) {
-    constexpr int kOp = 4 * 2 * NP * kUnit;   // one operand's share of a stage
-    __shared__ __align__(1024) uint8_t st0[2 * kOp];
-    __shared__ __align__(1024) uint8_t st1[2 * kOp];
-    const int HT = H / kTileH, hper = (HT + 7) / 8;
-    const int xcd = blockIdx.x & 7, rest = blockIdx.x >> 3;
-    const int ht = xcd * hper + rest % hper, tt = rest / hper;
-    if (ht >= HT) return;
+__global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp, int T,
+                                                int H, int EC, int TG, DxTiles tiles, void *__restrict__ dx) {
+    constexpr int RS = NP == 2 ? 3 : 2;
+    constexpr int kOpA = 8 * 2 * NP * kUnit, kOpB = 4 * 2 * NP * kUnit;
+    constexpr int kFills = 3 * NP;   // per wave and step
+    __shared__ __align__(1024) uint8_t st0[kOpA + kOpB];
+    __shared__ __align__(1024) uint8_t st1[kOpA + kOpB];
+    __shared__ __align__(1024) uint8_t st2[RS == 3 ? kOpA + kOpB : 16];
+    const int total = tiles.HT * tiles.TT, per = (total + 7) / 8;
+    const int xcd = blockIdx.x & 7, slots = gridDim.x >> 3;
+    const int last = (xcd + 1) * per < total ? (xcd + 1) * per : total;
+    const int first = xcd * per + (blockIdx.x >> 3);
+    if (first >= last) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int HG = H / 32, S = EC / 2;
-    // fills: wave w copies group w of each operand (2 chunks x NP units)
-    const int tgrp = 4 * tt + wave < TG ? 4 * tt + wave : TG - 1;
-    const uint8_t *asrc = wrp + (size_t)(4 * ht + wave < HG ? 4 * ht + wave : HG - 1) * EC * NP * kUnit;
-    const uint8_t *bsrc = dza + (size_t)tgrp * EC * NP * kUnit;
-    auto fill = [&](uint8_t *st, int s) {
+
+    // fill cursor: tile and step of the next fill (it stays on the last step
+    // once everything is on its way; those fills land in a stage nobody reads)
+    int ftile = first, fs = 0;
+    const uint8_t *fa, *fb;
+    auto seek = [&](int tile) {
+        int ht, tt;
+        tiles.at(tile, ht, tt);
+        const int hg = 8 * ht + wave < HG ? 8 * ht + wave : HG - 1;
+        const int tg = 4 * tt + (wave >> 1) < TG ? 4 * tt + (wave >> 1) : TG - 1;
+        fa = wrp + (size_t)hg * EC * NP * kUnit;
+        fb = dza + ((size_t)tg * EC + (wave & 1)) * NP * kUnit;
+    };
+    seek(first);
+    auto fill = [&](uint8_t *st) {
 #pragma unroll
-        for (int u = 0; u < 2 * NP; ++u) {
-            fill_unit(asrc + ((size_t)s * 2 * NP + u) * kUnit, st + (wave * 2 * NP + u) * kUnit);
-            fill_unit(bsrc + ((size_t)s * 2 * NP + u) * kUnit, st + kOp + (wave * 2 * NP + u) * kUnit);
+        for (int u = 0; u < 2 * NP; ++u) fill_unit(fa + u * kUnit, st + (wave * 2 * NP + u) * kUnit);
+#pragma unroll
+        for (int u = 0; u < NP; ++u) fill_unit(fb + u * kUnit, st + kOpA + (wave * NP + u) * kUnit);
+        if (fs + 1 < S) {
+            ++fs;
+            fa += 2 * NP * kUnit;
+            fb += 2 * NP * kUnit;
+        } else if (ftile + slots < last) {
+            ftile += slots;
+            fs = 0;
+            seek(ftile);
         }
     };
-    const int wr = wave & 1, wc = wave >> 1;   // this wave's 64 hidden columns and 64 tokens
+    const int wr = wave >> 1, wc = wave & 1;   // this wave's 64 hidden columns and 64 tokens
     f32x16 acc[2][2];
+    auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    auto step = [&](const uint8_t *cur) {
+                for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    };
+    clear();
+    int tile = first, s = 0;
+    auto store = [&]() {
+        int ht, tt;
+        tiles.at(tile, ht, tt);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = kTileT * tt + 64 * wc + 32 * j + (lane & 31);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
+                    const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
+                                v3 = acc[i][j][4 * q + 3];
+                    const size_t at = (size_t)t * H + h;
+                    if (t < T && h < H) {
+                        if constexpr (__is_same(DX, float))
+                            *reinterpret_cast<float4 *>(static_cast<float *>(dx) + at) = make_float4(v0, v1, v2, v3);
+                        else
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dx) + at) =
+                                make_uint2(bf16x2_bits(v0, v1), bf16x2_bits(v2, v3));
+                    }
+                }
+        }
+    };
+    // One step: the stage's fills are in once at most those of the RS - 2
+    // later steps are outstanding (stores in between only make the wait
+    // longer); after the barrier everyone's are, and everyone is done with the
+    // stage of the step before, which is filled next.
+    auto step = [&](const uint8_t *cur, uint8_t *next) {
+        fill_barrier<(RS - 2) * kFills>();
+        fill(next);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             bf16x8 A[2][NP], B[2][NP];
@@ -315,7 +410,7 @@ __global__ __launch_bounds__(256) void route_dx(const uint8_t *__restrict__ dza,
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     A[i][p] = lds_unit(cur + (((2 * wr + i) * 2 + c) * NP + p) * kUnit);
-                    B[i][p] = lds_unit(cur + kOp + (((2 * wc + i) * 2 + c) * NP + p) * kUnit);
+                    B[i][p] = lds_unit(cur + kOpA + (((2 * wc + i) * 2 + c) * NP + p) * kUnit);
                 }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
@@ -326,61 +421,45 @@ __global__ __launch_bounds__(256) void route_dx(const uint8_t *__restrict__ dza,
 #pragma unroll
                         for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[i][p], B[j][q], acc[i][j]);
         }
+        if (++s == S) {
+            store();
+            clear();
+            s = 0;
+            tile += slots;
+        }
+        return tile < last;
     };
-    fill(st0, 0);
-    for (int s = 0; s < S; s += 2) {
-        wait_vmem();
-        __syncthreads();
-        if (s + 1 < S) fill(st1, s + 1);
-        step(st0);
-        if (s + 1 >= S) break;
-        wait_vmem();
-        __syncthreads();
-        if (s + 2 < S) fill(st0, s + 2);
-        step(st1);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int t = kTileT * tt + 64 * wc + 32 * j + (lane & 31);
-        if (t >= T) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
-                const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
-                            v3 = acc[i][j][4 * q + 3];
-                const size_t at = (size_t)t * H + h;
-                if constexpr (__is_same(DX, float))
-                    *reinterpret_cast<float4 *>(static_cast<float *>(dx) + at) = make_float4(v0, v1, v2, v3);
-                else
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dx) + at) =
-                        make_uint2(bf16x2_bits(v0, v1), bf16x2_bits(v2, v3));
-            }
+    fill(st0);
+    if constexpr (RS == 3) {
+        fill(st1);
+        while (step(st0, st2) && step(st1, st0) && step(st2, st1)) {}
+    } else {
+        while (step(st0, st1) && step(st1, st0)) {}
     }
 }
 
 // ----------------------------------- dWr -----------------------------------
 // Tokens of one thread's piece of a step: two hidden columns x eight tokens,
-// as two bf16 per dword (x) or two codes and their scale (checkpoint).
+// as two bf16 per dword (x) or two codes and their scale (checkpoint).  Every
+// row is a buffer of its own with the row's length, or none for a row that
+// takes no part (past the end, or masked): such rows and columns past H read
+// as zeros, whatever is stored there.
 template <bool MX>
 struct XPiece {
     uint32_t v[8];
     uint32_t s[MX ? 8 : 1];
-    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, int t1, int h) {
+    // rows t0 .. t0 + 7 (uniform), bit i of `valid` for row t0 + i; column h
+    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, int h) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int t = t0 + i;
-            const bool in = t < t1 && !(a.mask && a.mask[t] == 0);   // past the end or masked: 0 whatever is stored
-            const size_t at = (size_t)(in ? t : 0) * a.H + h;
+            const uint32_t in = (valid >> i) & 1u;
+            const size_t row = (size_t)(t0 + i) * a.H;
             if constexpr (MX) {
-                const uint32_t c = *reinterpret_cast<const uint16_t *>(a.codes + at);
-                const uint32_t sc = a.scales[at >> 5];
-                v[i] = in ? c : 0u;
-                s[i] = in ? sc : 127u;
+                v[i] = __builtin_amdgcn_raw_buffer_load_b16(buffer_rsrc(a.codes + row, in ? a.H : 0), h, 0, 0);
+                s[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(a.scales + (row >> 5), in ? a.H >> 5 : 0),
+                                                           h >> 5, 0, 0);
             } else {
-                const uint32_t c = *reinterpret_cast<const uint32_t *>(a.x + at);
-                v[i] = in ? c : 0u;
+                v[i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(a.x + row, in ? 2 * a.H : 0), 2 * h, 0, 0);
             }
         }
     }
@@ -413,19 +492,26 @@ struct XPiece {
 // writing the slots 2 l (then 2 l + 1) hits every bank group once per 8 lanes.
 __device__ __forceinline__ int x_slot(int s) { return 16 * (s ^ ((s >> 3) & 1)); }
 
-// dWr tile: 128 experts x 128 hidden columns over one split of the tokens in
-// steps of 32.  MFMA rows = experts (dz units, copied to LDS), columns =
-// hidden columns (x, transposed in registers on its way to LDS).
+// dWr = dz^T x: 128 experts x 256 hidden columns per block over one split of
+// the tokens in steps of 32, eight waves of 64 x 64.  MFMA rows = experts (dz
+// units, copied to LDS), columns = hidden columns (x, transposed in registers
+// on its way to LDS).  A ring of three LDS stages (120 KB): at step s the dz
+// units of step s + 2 start into LDS and the x rows of step s + 2 into
+// registers, and the x rows of step s + 1, loaded a step ago, are written to
+// its stage.
 // out: the split's partial [E][H], or dWr itself with one split.
 template <bool MX>
-__global__ __launch_bounds__(256) void route_dwr(RouteBwdArgs a, const uint8_t *__restrict__ dzt, int EG, int steps,
-                                                 int splits, float *__restrict__ out) {
-    constexpr int kA = 4 * 2 * 3 * kUnit, kB = 4 * 2 * kUnit;
+__global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *__restrict__ dzt,
+                                                 const uint32_t *__restrict__ valid, int EG, int steps, int splits,
+                                                 float *__restrict__ out) {
+    constexpr int kA = 4 * 2 * 3 * kUnit, kB = 8 * 2 * kUnit;
+    constexpr int kLoads = 3 + (MX ? 16 : 8);   // per wave and step: dz units, x rows
     __shared__ __align__(1024) uint8_t st0[kA + kB];
     __shared__ __align__(1024) uint8_t st1[kA + kB];
+    __shared__ __align__(1024) uint8_t st2[kA + kB];
     const int H = a.H, E = a.E;
     const int net = (E + kTileE - 1) / kTileE;
-    const int nht = H / kTileH;
+    const int nht = (H + kTileH - 1) / kTileH;
     // the expert tiles of one (split, hidden tile) are consecutive on one XCD
     // (they read the same x), and an XCD stays with few splits (the same dz)
     const int total = net * nht * splits, per = (total + 7) / 8;
@@ -435,26 +521,25 @@ __global__ __launch_bounds__(256) void route_dwr(RouteBwdArgs a, const uint8_t *
     const int per_split = (steps + splits - 1) / splits;
     const int s0 = sp * per_split, s1 = s0 + per_split < steps ? s0 + per_split : steps;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int eg = 4 * et + wave < EG ? 4 * et + wave : EG - 1;
+    // dz units of this wave: expert group wave / 2 of the tile, chunk wave % 2
+    const int eg = 4 * et + (wave >> 1) < EG ? 4 * et + (wave >> 1) : EG - 1;
     auto fill_a = [&](uint8_t *st, int s) {
+        const uint8_t *src = dzt + ((size_t)(2 * s + (wave & 1)) * EG + eg) * 3 * kUnit;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-                fill_unit(dzt + (((size_t)(2 * s + c) * EG + eg) * 3 + p) * kUnit,
-                          st + ((wave * 2 + c) * 3 + p) * kUnit);
+        for (int p = 0; p < 3; ++p) fill_unit(src + p * kUnit, st + (wave * 3 + p) * kUnit);
     };
-    // x piece of this thread: hidden columns 2 lane, 2 lane + 1 of the tile,
-    // tokens 8 wave .. +7 of the step (chunk wave / 2, lane half wave % 2)
-    const int h = kTileH * ht + 2 * lane;
-    uint8_t *const xdst0 = st0 + kA, *const xdst1 = st1 + kA;
-    const int xunit = ((lane >> 4) * 2 + (wave >> 1)) * kUnit;
-    const int slot = ((2 * lane) & 31) + 32 * (wave & 1);
-    auto put_x = [&](uint8_t *dst, XPiece<MX> &x) {
+    // x piece of this thread: hidden columns 128 (wave % 2) + 2 lane, + 1 of
+    // the tile, tokens 8 (wave / 2) .. +7 of the step
+    const int h = kTileH * ht + 128 * (wave & 1) + 2 * lane;
+    const int oct = wave >> 1;
+    const int xunit = ((4 * (wave & 1) + (lane >> 4)) * 2 + (oct >> 1)) * kUnit;
+    const int slot = ((2 * lane) & 31) + 32 * (oct & 1);
+    const int xlo = kA + xunit + x_slot(slot), xhi = kA + xunit + x_slot(slot + 1);
+    auto put_x = [&](uint8_t *st, XPiece<MX> &x) {
         uint4 lo, hi;
         x.pieces(lo, hi);
-        *reinterpret_cast<uint4 *>(dst + xunit + x_slot(slot)) = lo;
-        *reinterpret_cast<uint4 *>(dst + xunit + x_slot(slot + 1)) = hi;
+        *reinterpret_cast<uint4 *>(st + xlo) = lo;
+        *reinterpret_cast<uint4 *>(st + xhi) = hi;
     };
     const int wr = wave & 1, wc = wave >> 1;   // this wave's 64 experts and 64 hidden columns
     f32x16 acc[2][2];
@@ -464,7 +549,19 @@ __global__ __launch_bounds__(256) void route_dwr(RouteBwdArgs a, const uint8_t *
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    auto step = [&](const uint8_t *cur) {
+    uint32_t ok2 = 0;   // the tokens that count in the step whose x rows are loaded next
+    // Step s: computes from `cur`, fills `nn` (s + 2), writes x of s + 1 to
+    // `next`.  Steps past the end load the last one again, into a stage that
+    // nobody reads, so that the counts below hold to the end.
+    auto step = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn, int s) {
+        // all but the newest step's loads are done: the dz units of step s;
+        // the wait on LDS covers its x rows.  After the barrier that holds for
+        // every wave, and every wave is done with step s - 1, whose stage nn is
+        fill_barrier<kLoads>();
+        const int n = s + 2 < s1 ? s + 2 : s1 - 1;
+        fill_a(nn, n);
+        xnn.load(a, kStepK * n + 8 * oct, ok2 >> (8 * oct), h);
+        ok2 = valid[s + 3 < s1 ? s + 3 : s1 - 1];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             bf16x8 A[2][3], B[2];
@@ -481,36 +578,32 @@ __global__ __launch_bounds__(256) void route_dwr(RouteBwdArgs a, const uint8_t *
 #pragma unroll
                     for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[i][p], B[j], acc[i][j]);
         }
+        put_x(next, xnext);
     };
-    XPiece<MX> x;
     if (s0 < s1) {
+        XPiece<MX> x0, x1;
+        const int n = s0 + 1 < s1 ? s0 + 1 : s1 - 1;
+        const uint32_t ok0 = valid[s0], ok1 = valid[n];
+        ok2 = valid[s0 + 2 < s1 ? s0 + 2 : s1 - 1];
         fill_a(st0, s0);
-        x.load(a, kStepK * s0 + 8 * wave, a.T, h);
-        put_x(xdst0, x);
-    }
-    for (int s = s0; s < s1; s += 2) {
-        wait_vmem();
-        __syncthreads();
-        if (s + 1 < s1) {
-            fill_a(st1, s + 1);
-            x.load(a, kStepK * (s + 1) + 8 * wave, a.T, h);
+        x0.load(a, kStepK * s0 + 8 * oct, ok0 >> (8 * oct), h);
+        fill_a(st1, n);
+        x1.load(a, kStepK * n + 8 * oct, ok1 >> (8 * oct), h);
+        put_x(st0, x0);
+        for (int s = s0; s < s1; s += 6) {   // one exit: with one per step every step's tile would be kept apart
+            step(st0, st1, st2, x1, x0, s);
+            if (s + 1 < s1) step(st1, st2, st0, x0, x1, s + 1);
+            if (s + 2 < s1) step(st2, st0, st1, x1, x0, s + 2);
+            if (s + 3 < s1) step(st0, st1, st2, x0, x1, s + 3);
+            if (s + 4 < s1) step(st1, st2, st0, x1, x0, s + 4);
+            if (s + 5 < s1) step(st2, st0, st1, x0, x1, s + 5);
         }
-        step(st0);
-        if (s + 1 >= s1) break;
-        put_x(xdst1, x);
-        wait_vmem();
-        __syncthreads();
-        if (s + 2 < s1) {
-            fill_a(st0, s + 2);
-            x.load(a, kStepK * (s + 2) + 8 * wave, a.T, h);
-        }
-        step(st1);
-        if (s + 2 < s1) put_x(xdst0, x);
     }
     float *const dst = out + (splits > 1 ? (size_t)sp * E * H : 0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int hc = kTileH * ht + 64 * wc + 32 * j + (lane & 31);
+        if (hc >= H) continue;
         const float sc = splits == 1 && a.q_weight ? a.q_weight[hc] : 1.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -522,9 +615,27 @@ __global__ __launch_bounds__(256) void route_dwr(RouteBwdArgs a, const uint8_t *
     }
 }
 
-// dWr from the splits' partials, in split order, times the checkpoint's column weight.
-__global__ __launch_bounds__(256) void route_dwr_sum(const float4 *__restrict__ part, int splits, size_t n4, int H4,
-                                                     const float4 *__restrict__ q_weight, float4 *__restrict__ out) {
+// The sums over blocks.  Blocks [0, n_dwr): dWr from the splits' partials, in
+// split order, times the checkpoint's column weight; the others: 64 columns of
+// db each from the token groups' parts, four interleaved chains.
+__global__ __launch_bounds__(256) void route_sums(const float4 *__restrict__ part, int splits, size_t n4, int H4,
+                                                  const float4 *__restrict__ q_weight, float4 *__restrict__ dwr,
+                                                  int n_dwr, const float *__restrict__ dbp, int TG, int E,
+                                                  float *__restrict__ db) {
+    if ((int)blockIdx.x >= n_dwr) {
+        __shared__ float lds[4][64];
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int e = 64 * (blockIdx.x - n_dwr) + lane;
+        float s = 0.f;
+        if (e < E) {
+#pragma unroll 16
+            for (int r = wave; r < TG; r += 4) s += dbp[(size_t)r * E + e];
+        }
+        lds[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && e < E) db[e] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+        return;
+    }
     const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n4) return;
     float4 s = part[i];
@@ -542,7 +653,7 @@ __global__ __launch_bounds__(256) void route_dwr_sum(const float4 *__restrict__ 
         s.z *= w.z;
         s.w *= w.w;
     }
-    out[i] = s;
+    dwr[i] = s;
 }
 
 // Zeros (a kernel, so that the call may be captured in a graph).
@@ -729,23 +840,28 @@ hipError_t launch_few(const RouteBwdArgs &a, char *ws, hipStream_t st) {
 }
 
 template <int NP>
-void launch_dz(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
-    uint8_t *dza = a.dx ? reinterpret_cast<uint8_t *>(ws + w.dza) : nullptr;
-    uint8_t *dzt = a.dwr ? reinterpret_cast<uint8_t *>(ws + w.dzt) : nullptr;
+void launch_operands(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
+    uint8_t *u = reinterpret_cast<uint8_t *>(ws);
+    uint8_t *dza = a.dx ? u + w.dza : nullptr, *dzt = a.dwr ? u + w.dzt : nullptr, *wrp = u + w.wrp;
+    uint32_t *valid = reinterpret_cast<uint32_t *>(ws + w.valid);
     float *dbp = a.db ? reinterpret_cast<float *>(ws + w.dbp) : nullptr;
-    const dim3 g(w.tg), b(512);
-#define MOE_DZ(N) MOE_LAUNCH("route_dz", (route_dz<N, NP>), g, b, 0, st, a, dza, dzt, dbp, w.ec, w.eg)
-    MOE_BY_NPL(a.E, MOE_DZ)
-#undef MOE_DZ
+    const dim3 g(w.tg + (a.dx ? w.eg * ((a.H + 255) / 256) : 0)), b(1024);
+#define MOE_OPS(N) \
+    MOE_LAUNCH("route_operands", (route_operands<N, NP>), g, b, 0, st, a, dza, dzt, wrp, valid, dbp, w.tg, w.ec, w.eg)
+    MOE_BY_NPL(a.E, MOE_OPS)
+#undef MOE_OPS
 }
 
 template <int NP, typename DX>
 void launch_dx(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
-    uint8_t *wrp = reinterpret_cast<uint8_t *>(ws + w.wrp);
-    MOE_LAUNCH("route_wr_units", route_wr_units<NP>, dim3(a.H / 64, w.eg), dim3(256), 0, st, a.wr, a.E, a.H, wrp, w.ec);
-    const int hper = (a.H / kTileH + 7) / 8, tt = (a.T + kTileT - 1) / kTileT;
-    MOE_LAUNCH("route_dx", (route_dx<NP, DX>), dim3(8 * hper * tt), dim3(256), 0, st,
-               reinterpret_cast<const uint8_t *>(ws + w.dza), wrp, a.T, a.H, w.ec, w.tg, a.dx);
+    DxTiles t;
+    t.HT = (a.H + kTileH - 1) / kTileH;
+    t.TT = (a.T + kTileT - 1) / kTileT;
+    t.hper = (t.HT + 7) / 8;
+    const int per = (t.HT * t.TT + 7) / 8, slots = per < kCus / 8 ? per : kCus / 8;
+    MOE_LAUNCH("route_dx", (route_dx<NP, DX>), dim3(8 * slots), dim3(512), 0, st,
+               reinterpret_cast<const uint8_t *>(ws + w.dza), reinterpret_cast<const uint8_t *>(ws + w.wrp), a.T, a.H,
+               w.ec, w.tg, t, a.dx);
 }
 
 }  // namespace
@@ -766,33 +882,34 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st
     }
     if (a.T <= kFewTokens) return launch_few(a, ws, st);
     if (planes == 3)
-        launch_dz<3>(a, w, ws, st);
+        launch_operands<3>(a, w, ws, st);
     else
-        launch_dz<2>(a, w, ws, st);
+        launch_operands<2>(a, w, ws, st);
     if (a.dx) {
         if (planes == 3)
             launch_dx<3, float>(a, w, ws, st);
         else
             launch_dx<2, Bf16>(a, w, ws, st);
     }
+    float *part = reinterpret_cast<float *>(ws + w.dwp);
     if (a.dwr) {
         const uint8_t *dzt = reinterpret_cast<const uint8_t *>(ws + w.dzt);
-        float *part = reinterpret_cast<float *>(ws + w.dwp);
+        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ws + w.valid);
         float *out = w.splits > 1 ? part : a.dwr;
-        const int total = ((a.E + kTileE - 1) / kTileE) * (a.H / kTileH) * w.splits;
+        const int total = ((a.E + kTileE - 1) / kTileE) * ((a.H + kTileH - 1) / kTileH) * w.splits;
         const dim3 g(8 * ((total + 7) / 8));
         if (a.x == nullptr)
-            MOE_LAUNCH("route_dwr", route_dwr<true>, g, dim3(256), 0, st, a, dzt, w.eg, w.tg, w.splits, out);
+            MOE_LAUNCH("route_dwr", route_dwr<true>, g, dim3(512), 0, st, a, dzt, valid, w.eg, w.tg, w.splits, out);
         else
-            MOE_LAUNCH("route_dwr", route_dwr<false>, g, dim3(256), 0, st, a, dzt, w.eg, w.tg, w.splits, out);
-        if (w.splits > 1) {
-            const size_t n4 = ne / 4;
-            MOE_LAUNCH("route_dwr_sum", route_dwr_sum, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st,
-                       reinterpret_cast<const float4 *>(part), w.splits, n4, a.H / 4,
-                       reinterpret_cast<const float4 *>(a.q_weight), reinterpret_cast<float4 *>(a.dwr));
-        }
+            MOE_LAUNCH("route_dwr", route_dwr<false>, g, dim3(512), 0, st, a, dzt, valid, w.eg, w.tg, w.splits, out);
     }
-    if (a.db) return launch_column_sum("db_sum", reinterpret_cast<const float *>(ws + w.dbp), w.tg, a.E, a.db, st);
+    const size_t n4 = ne / 4;
+    const int n_dwr = a.dwr && w.splits > 1 ? (int)((n4 + 255) / 256) : 0, n_db = a.db ? (a.E + 63) / 64 : 0;
+    if (n_dwr + n_db > 0)
+        MOE_LAUNCH("route_sums", route_sums, dim3(n_dwr + n_db), dim3(256), 0, st,
+                   reinterpret_cast<const float4 *>(part), w.splits, n4, a.H / 4,
+                   reinterpret_cast<const float4 *>(a.q_weight), reinterpret_cast<float4 *>(a.dwr), n_dwr,
+                   reinterpret_cast<const float *>(ws + w.dbp), w.tg, a.E, a.db);
     return hipGetLastError();
 }
 
