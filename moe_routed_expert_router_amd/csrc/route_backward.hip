@@ -9,12 +9,18 @@
 //   plus the caller's dz_in, then
 //     dx = dz Wr,   dWr = dz^T x,   db = sum over tokens of dz.
 //
-// The two products run on the 32x32x16 bf16 MFMA.  dz and Wr are fp32: each
-// is split into bf16 terms (hi + mid + lo carries 24 bits), x is bf16 (or an
-// 8-bit checkpoint, exact in bf16).  dWr takes all three terms of dz (every
-// product exact in fp32, only the accumulation rounds); dx takes hi hi + hi lo
-// + lo hi where it is stored as bf16 (error 2^-16 against the 2^-9 of the
-// store) and the six products above 2^-24 where it is stored as fp32.
+// The two products run on the 32x32x16 MFMAs; their fp32 factors enter as
+// 16-bit terms.
+//   dx: fp16 terms.  Every row of dz (a token) and every column of Wr is first
+//     scaled by the power of two that brings its largest magnitude to [2^14,
+//     2^15), so nothing overflows and what lies below fp16's least step (2^-24)
+//     is under 2^-39 of the row's largest; the product is scaled back.  One
+//     term (2^-11 of the value) where dx is stored as bf16 (2^-8); hi hi + hi lo
+//     + lo hi of two terms (2^-22) where it is stored as fp32.
+//   dWr: bf16 terms of dz, hi + mid + lo (24 bits), times x, which is bf16 (or
+//     an 8-bit checkpoint, exact in bf16): every product is exact in fp32 and
+//     only the accumulation rounds.  (fp16 would do with two terms, but x has no
+//     bound that fits fp16 without a pass over it.)
 //
 // Operand layout.  The launches before the products write every operand as
 // units of 1 KB in the MFMA's own lane order: a unit holds 32 rows x 16 values
@@ -32,8 +38,8 @@ constexpr int kDzTok = 32;    // tokens per block of route_dz
 
 // ------------------------------- workspace ---------------------------------
 struct RouteWs {
-    int tg, ec, eg, hg;   // groups: 32 tokens, 16 experts (even), 32 experts, 32 hidden columns
-    size_t dza, dzt, wrp, valid, dbp, dwp, total;
+    int tg, ec, eg, hg;   // groups: 32 tokens, 16 experts (a multiple of 4), 32 experts, 32 hidden columns
+    size_t tscale, hscale, dza, dzt, wrp, valid, dbp, dwp, total;
     int splits;
 };
 
@@ -53,11 +59,11 @@ int dw_splits(int T, int H, int E) {
     return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
 }
 
-RouteWs route_ws(int T, int H, int E, int planes) {
+RouteWs route_ws(int T, int H, int E, int terms) {
     RouteWs w;
     w.tg = (T + 31) / 32;
     w.eg = (E + 31) / 32;
-    w.ec = 2 * w.eg;
+    w.ec = 4 * ((E + 63) / 64);
     w.hg = H / 32;
     w.splits = dw_splits(T, H, E);
     size_t at = 0;
@@ -66,9 +72,11 @@ RouteWs route_ws(int T, int H, int E, int planes) {
         at += WsLayout::up(n);
         return r;
     };
-    w.dza = take((size_t)w.tg * w.ec * planes * kUnit);
+    w.tscale = take((size_t)w.tg * 32 * 4);
+    w.hscale = take((size_t)H * 4);
+    w.dza = take((size_t)w.tg * w.ec * terms * kUnit);
     w.dzt = take((size_t)w.tg * 2 * w.eg * 3 * kUnit);
-    w.wrp = take((size_t)w.hg * w.ec * planes * kUnit);
+    w.wrp = take((size_t)w.hg * w.ec * terms * kUnit);
     w.valid = take((size_t)w.tg * 4);
     w.dbp = take((size_t)w.tg * E * 4);
     w.dwp = take((size_t)w.splits * E * H * 4);
@@ -109,6 +117,32 @@ __device__ __forceinline__ void split8(const float *v, uint4 *o) {
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) o[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// The same with fp16 terms of scaled values (finite ones below 2^15).
+template <int NP>
+__device__ __forceinline__ void split8_f16(const float *v, uint4 *o) {
+    uint32_t w[NP][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const _Float16 x = (_Float16)a, y = (_Float16)b;
+            w[p][i] = (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+            // a non-finite value stays in the first term alone
+            a = fabsf(a) < INFINITY ? a - (float)x : 0.f;
+            b = fabsf(b) < INFINITY ? b - (float)y : 0.f;
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) o[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// Exponent s with 2^s max in [2^14, 2^15); 0 for a zero or non-finite maximum.
+__device__ __forceinline__ int scale_exponent(float max) {
+    const int e = (int)((__float_as_uint(max) >> 23) & 255u);
+    return max == 0.f || e == 255 ? 0 : 14 + 127 - e;
 }
 
 // --------------------------------- dz --------------------------------------
@@ -179,54 +213,60 @@ __device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[
     }
 }
 
-// Wr [E][H] as units (32 hidden columns, 16 experts): 256 columns of one
-// 32-expert group, through an LDS tile; each of the 16 waves leaves one unit.
-constexpr int kWrPitch = 257;
+// 32 columns of Wr [E][H] as scaled units (32 hidden columns, 16 experts):
+// first the columns' maxima, then, from the cache, the values.
 template <int NP>
-__device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int EC, int block, float *tile) {
+__device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int32_t *__restrict__ hscale, int EC, int hg,
+                         float *lds) {
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int HB = (a.H + 255) / 256, h0 = 256 * (block % HB), eg = block / HB;
-    {
-        const int c = tid & 255, h = h0 + c < a.H ? h0 + c : a.H - 1;
+    const float *col = a.wr + 32 * hg + (lane & 31);
+    float m = 0.f;
+#pragma unroll 4
+    for (int e = tid >> 5; e < a.E; e += 32) {
+        // NaN and infinities count as infinite: the column is not scaled
+        const float v = fabsf(col[(size_t)e * a.H]);
+        m = v < INFINITY ? fmaxf(m, v) : INFINITY;
+    }
+    lds[tid] = m;
+    __syncthreads();
+    m = 0.f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) m = fmaxf(m, lds[32 * r + (lane & 31)]);
+    const int sc = scale_exponent(m);
+    if (tid < 32) hscale[32 * hg + tid] = sc;
+    for (int ec = wave; ec < EC; ec += 16) {
         float v[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int e = 32 * eg + (tid >> 8) + 4 * r;
-            v[r] = e < a.E ? a.wr[(size_t)e * a.H + h] : 0.f;
+        for (int i = 0; i < 8; ++i) {
+            const int e = 16 * ec + 8 * (lane >> 5) + i;
+            v[i] = e < a.E ? ldexpf(col[(size_t)e * a.H], sc) : 0.f;
         }
+        uint4 o[NP];
+        split8_f16<NP>(v, o);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) tile[((tid >> 8) + 4 * r) * kWrPitch + c] = v[r];
+        for (int q = 0; q < NP; ++q)
+            *reinterpret_cast<uint4 *>(out + (((size_t)hg * EC + ec) * NP + q) * kUnit + 16 * lane) = o[q];
     }
-    __syncthreads();
-    const int hg = wave >> 1, ch = wave & 1;
-    if (h0 + 32 * hg >= a.H) return;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = tile[(16 * ch + 8 * (lane >> 5) + i) * kWrPitch + 32 * hg + (lane & 31)];
-    uint4 o[NP];
-    split8<NP>(v, o);
-    const size_t unit = (size_t)(h0 / 32 + hg) * EC + 2 * eg + ch;
-#pragma unroll
-    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint4 *>(out + (unit * NP + q) * kUnit + 16 * lane) = o[q];
 }
 
 // The operands of both products.  Blocks [0, tg): 32 tokens each, a wave per
 // token at a time: dz of the row in registers, then in an LDS tile from which
 // it leaves in both operand orders (token rows for dx, expert rows for dWr)
 // and as the block's part of db; tokens past T and masked tokens have dz = 0.
-// Blocks past tg (for dx): the router weight.
+// Blocks past tg (for dx): 32 columns of the router weight each.
 template <int NPL, int NP>
 __global__ __launch_bounds__(1024) void route_operands(RouteBwdArgs a, uint8_t *__restrict__ dza,
                                                        uint8_t *__restrict__ dzt, uint8_t *__restrict__ wrp,
+                                                       int32_t *__restrict__ tscale, int32_t *__restrict__ hscale,
                                                        uint32_t *__restrict__ valid, float *__restrict__ dbp, int TG,
                                                        int EC, int EG) {
     constexpr int kPitch = 64 * NPL + 4;
-    constexpr int kDzLds = kDzTok * kPitch, kWrLds = 32 * kWrPitch;
-    __shared__ __align__(16) float lds[kDzLds > kWrLds ? kDzLds : kWrLds];
+    __shared__ __align__(16) float lds[kDzTok * kPitch];   // at least the 1024 that wr_units uses
+    __shared__ int tsc[kDzTok];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
     const int tgrp = blockIdx.x, tok0 = tgrp * kDzTok;
     if (tgrp >= TG) {
-        wr_units<NP>(a, wrp, EC, tgrp - TG, lds);
+        wr_units<NP>(a, wrp, hscale, EC, tgrp - TG, lds);
         return;
     }
     float(*tile)[kPitch] = reinterpret_cast<float(*)[kPitch]>(lds);
@@ -235,9 +275,20 @@ __global__ __launch_bounds__(1024) void route_operands(RouteBwdArgs a, uint8_t *
         dz_row<NPL>(a, tok0 + wave, v[0]);
         dz_row<NPL>(a, tok0 + wave + 16, v[1]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+            float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) tile[wave + 16 * r][lane + 64 * i] = v[r][i];
+            for (int i = 0; i < NPL; ++i) {
+                tile[wave + 16 * r][lane + 64 * i] = v[r][i];
+                const float u = fabsf(v[r][i]);
+                m = u < INFINITY ? fmaxf(m, u) : INFINITY;
+            }
+            const int sc = scale_exponent(wave_max(m));
+            if (lane == 0) {
+                tsc[wave + 16 * r] = sc;
+                if (dza) tscale[tok0 + wave + 16 * r] = sc;
+            }
+        }
     }
     if (wave == 0) {   // a bit per token of the group that counts
         const int t = tok0 + lane;
@@ -254,13 +305,14 @@ __global__ __launch_bounds__(1024) void route_operands(RouteBwdArgs a, uint8_t *
     // token rows: the 16-expert chunk ec of this token group, lane (token
     // l % 32, experts 8 (l / 32) .. +7); columns E .. 16 EC - 1 of the tile are 0
     if (dza) {
+        const int sc = tsc[lane & 31];
         for (int ec = wave; ec < EC; ec += 16) {
             const float *p = &tile[lane & 31][16 * ec + 8 * (lane >> 5)];
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p[i];
+            for (int i = 0; i < 8; ++i) v[i] = ldexpf(p[i], sc);
             uint4 o[NP];
-            split8<NP>(v, o);
+            split8_f16<NP>(v, o);
 #pragma unroll
             for (int q = 0; q < NP; ++q)
                 *reinterpret_cast<uint4 *>(dza + (((size_t)tgrp * EC + ec) * NP + q) * kUnit + 16 * lane) = o[q];
@@ -285,8 +337,11 @@ __global__ __launch_bounds__(1024) void route_operands(RouteBwdArgs a, uint8_t *
 }
 
 // ----------------------------------- dx ------------------------------------
-__device__ __forceinline__ bf16x8 lds_unit(const uint8_t *p) {
-    return *reinterpret_cast<const bf16x8 *>(p + 16 * (threadIdx.x & 63));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+template <typename V>
+__device__ __forceinline__ V lds_unit(const uint8_t *p) {
+    return *reinterpret_cast<const V *>(p + 16 * (threadIdx.x & 63));
 }
 
 // One linear copy of a unit into LDS by this wave.
@@ -308,28 +363,29 @@ struct DxTiles {
 };
 
 // dx = dz Wr: 128 tokens x 256 hidden columns per tile, contraction over the
-// experts in steps of 32, eight waves of 64 x 64.  MFMA rows = hidden columns,
-// columns = tokens: a lane ends with four consecutive columns of one token.
-// One block per compute unit takes every 32nd tile of its XCD's share and runs
-// their steps as one sequence, so that the next tile's operands are on their
-// way while a tile is finished and stored.  LDS is a ring of RS stages (three
-// for two terms, two for three, 144 KB), filled RS - 1 steps ahead.
+// experts in steps of 64 (one term) or 32 (two), eight waves of 64 x 64.  MFMA
+// rows = hidden columns, columns = tokens: a lane ends with four consecutive
+// columns of one token.  One block per compute unit takes every 32nd tile of
+// its XCD's share and runs their steps as one sequence, so that the next
+// tile's operands are on their way while a tile is finished and stored.  LDS
+// is a ring of three 48 KB stages, filled two steps ahead.
 template <int NP, typename DX>
-__global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp, int T,
-                                                int H, int EC, int TG, DxTiles tiles, void *__restrict__ dx) {
-    constexpr int RS = NP == 2 ? 3 : 2;
-    constexpr int kOpA = 8 * 2 * NP * kUnit, kOpB = 4 * 2 * NP * kUnit;
-    constexpr int kFills = 3 * NP;   // per wave and step
+__global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp,
+                                                const int32_t *__restrict__ tscale, const int32_t *__restrict__ hscale,
+                                                int T, int H, int EC, int TG, DxTiles tiles, void *__restrict__ dx) {
+    constexpr int KC = 4 / NP;   // 16-expert chunks per step: KC NP = 4 units per group
+    constexpr int kOpA = 8 * 4 * kUnit, kOpB = 4 * 4 * kUnit;
+    constexpr int kFills = 6;    // per wave and step
     __shared__ __align__(1024) uint8_t st0[kOpA + kOpB];
     __shared__ __align__(1024) uint8_t st1[kOpA + kOpB];
-    __shared__ __align__(1024) uint8_t st2[RS == 3 ? kOpA + kOpB : 16];
+    __shared__ __align__(1024) uint8_t st2[kOpA + kOpB];
     const int total = tiles.HT * tiles.TT, per = (total + 7) / 8;
     const int xcd = blockIdx.x & 7, slots = gridDim.x >> 3;
     const int last = (xcd + 1) * per < total ? (xcd + 1) * per : total;
     const int first = xcd * per + (blockIdx.x >> 3);
     if (first >= last) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int HG = H / 32, S = EC / 2;
+    const int HG = H / 32, S = EC / KC;
 
     // fill cursor: tile and step of the next fill (it stays on the last step
     // once everything is on its way; those fills land in a stage nobody reads)
@@ -341,18 +397,18 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
         const int hg = 8 * ht + wave < HG ? 8 * ht + wave : HG - 1;
         const int tg = 4 * tt + (wave >> 1) < TG ? 4 * tt + (wave >> 1) : TG - 1;
         fa = wrp + (size_t)hg * EC * NP * kUnit;
-        fb = dza + ((size_t)tg * EC + (wave & 1)) * NP * kUnit;
+        fb = dza + ((size_t)tg * EC * NP + 2 * (wave & 1)) * kUnit;
     };
     seek(first);
     auto fill = [&](uint8_t *st) {
 #pragma unroll
-        for (int u = 0; u < 2 * NP; ++u) fill_unit(fa + u * kUnit, st + (wave * 2 * NP + u) * kUnit);
+        for (int u = 0; u < 4; ++u) fill_unit(fa + u * kUnit, st + (wave * 4 + u) * kUnit);
 #pragma unroll
-        for (int u = 0; u < NP; ++u) fill_unit(fb + u * kUnit, st + kOpA + (wave * NP + u) * kUnit);
+        for (int u = 0; u < 2; ++u) fill_unit(fb + u * kUnit, st + kOpA + (wave * 2 + u) * kUnit);
         if (fs + 1 < S) {
             ++fs;
-            fa += 2 * NP * kUnit;
-            fb += 2 * NP * kUnit;
+            fa += 4 * kUnit;
+            fb += 4 * kUnit;
         } else if (ftile + slots < last) {
             ftile += slots;
             fs = 0;
@@ -374,16 +430,27 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
     auto store = [&]() {
         int ht, tt;
         tiles.at(tile, ht, tt);
+        int4 hs[2][4];   // the scales of this lane's columns (past H: of the last ones, not stored)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
+                hs[i][q] = *reinterpret_cast<const int4 *>(hscale + (h < H ? h : H - 4));
+            }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int t = kTileT * tt + 64 * wc + 32 * j + (lane & 31);
+            const int ts = tscale[t < T ? t : T - 1];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
-                    const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
-                                v3 = acc[i][j][4 * q + 3];
+                    const float v0 = ldexpf(acc[i][j][4 * q], -ts - hs[i][q].x);
+                    const float v1 = ldexpf(acc[i][j][4 * q + 1], -ts - hs[i][q].y);
+                    const float v2 = ldexpf(acc[i][j][4 * q + 2], -ts - hs[i][q].z);
+                    const float v3 = ldexpf(acc[i][j][4 * q + 3], -ts - hs[i][q].w);
                     const size_t at = (size_t)t * H + h;
                     if (t < T && h < H) {
                         if constexpr (__is_same(DX, float))
@@ -395,22 +462,22 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
                 }
         }
     };
-    // One step: the stage's fills are in once at most those of the RS - 2
-    // later steps are outstanding (stores in between only make the wait
-    // longer); after the barrier everyone's are, and everyone is done with the
-    // stage of the step before, which is filled next.
+    // One step: the stage's fills are in once at most those of the next step
+    // are outstanding (stores in between only make the wait longer); after the
+    // barrier everyone's are, and everyone is done with the stage of the step
+    // before, which is filled next.
     auto step = [&](const uint8_t *cur, uint8_t *next) {
-        fill_barrier<(RS - 2) * kFills>();
+        fill_barrier<kFills>();
         fill(next);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            bf16x8 A[2][NP], B[2][NP];
+        for (int c = 0; c < KC; ++c) {
+            f16x8 A[2][NP], B[2][NP];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    A[i][p] = lds_unit(cur + (((2 * wr + i) * 2 + c) * NP + p) * kUnit);
-                    B[i][p] = lds_unit(cur + kOpA + (((2 * wc + i) * 2 + c) * NP + p) * kUnit);
+                    A[i][p] = lds_unit<f16x8>(cur + ((2 * wr + i) * 4 + c * NP + p) * kUnit);
+                    B[i][p] = lds_unit<f16x8>(cur + kOpA + ((2 * wc + i) * 4 + c * NP + p) * kUnit);
                 }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
@@ -419,7 +486,8 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[i][p], B[j][q], acc[i][j]);
+                        for (int j = 0; j < 2; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i][p], B[j][q], acc[i][j], 0, 0, 0);
         }
         if (++s == S) {
             store();
@@ -430,12 +498,8 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
         return tile < last;
     };
     fill(st0);
-    if constexpr (RS == 3) {
-        fill(st1);
-        while (step(st0, st2) && step(st1, st0) && step(st2, st1)) {}
-    } else {
-        while (step(st0, st1) && step(st1, st0)) {}
-    }
+    fill(st1);
+    while (step(st0, st2) && step(st1, st0) && step(st2, st1)) {}
 }
 
 // ----------------------------------- dWr -----------------------------------
@@ -568,7 +632,7 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int p = 0; p < 3; ++p) A[i][p] = lds_unit(cur + (((2 * wr + i) * 2 + c) * 3 + p) * kUnit);
+                for (int p = 0; p < 3; ++p) A[i][p] = lds_unit<bf16x8>(cur + (((2 * wr + i) * 2 + c) * 3 + p) * kUnit);
                 B[i] = *reinterpret_cast<const bf16x8 *>(cur + kA + ((2 * wc + i) * 2 + c) * kUnit + x_slot(lane));
             }
 #pragma unroll
@@ -842,12 +906,14 @@ hipError_t launch_few(const RouteBwdArgs &a, char *ws, hipStream_t st) {
 template <int NP>
 void launch_operands(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
     uint8_t *u = reinterpret_cast<uint8_t *>(ws);
+    int32_t *tscale = reinterpret_cast<int32_t *>(ws + w.tscale), *hscale = reinterpret_cast<int32_t *>(ws + w.hscale);
     uint8_t *dza = a.dx ? u + w.dza : nullptr, *dzt = a.dwr ? u + w.dzt : nullptr, *wrp = u + w.wrp;
     uint32_t *valid = reinterpret_cast<uint32_t *>(ws + w.valid);
     float *dbp = a.db ? reinterpret_cast<float *>(ws + w.dbp) : nullptr;
-    const dim3 g(w.tg + (a.dx ? w.eg * ((a.H + 255) / 256) : 0)), b(1024);
+    const dim3 g(w.tg + (a.dx ? w.hg : 0)), b(1024);
 #define MOE_OPS(N) \
-    MOE_LAUNCH("route_operands", (route_operands<N, NP>), g, b, 0, st, a, dza, dzt, wrp, valid, dbp, w.tg, w.ec, w.eg)
+    MOE_LAUNCH("route_operands", (route_operands<N, NP>), g, b, 0, st, a, dza, dzt, wrp, tscale, hscale, valid, dbp, w.tg, \
+               w.ec, w.eg)
     MOE_BY_NPL(a.E, MOE_OPS)
 #undef MOE_OPS
 }
@@ -860,20 +926,21 @@ void launch_dx(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st
     t.hper = (t.HT + 7) / 8;
     const int per = (t.HT * t.TT + 7) / 8, slots = per < kCus / 8 ? per : kCus / 8;
     MOE_LAUNCH("route_dx", (route_dx<NP, DX>), dim3(8 * slots), dim3(512), 0, st,
-               reinterpret_cast<const uint8_t *>(ws + w.dza), reinterpret_cast<const uint8_t *>(ws + w.wrp), a.T, a.H,
-               w.ec, w.tg, t, a.dx);
+               reinterpret_cast<const uint8_t *>(ws + w.dza), reinterpret_cast<const uint8_t *>(ws + w.wrp),
+               reinterpret_cast<const int32_t *>(ws + w.tscale), reinterpret_cast<const int32_t *>(ws + w.hscale), a.T,
+               a.H, w.ec, w.tg, t, a.dx);
 }
 
 }  // namespace
 
 size_t route_bwd_ws_bytes(int T, int H, int E) {
     if (T <= kFewTokens) return WsLayout::up((size_t)T * ((E + 7) & ~7) * 4);
-    return route_ws(T, H, E, 3).total;
+    return route_ws(T, H, E, 2).total;
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st) {
-    const int planes = a.dx_dtype == MOE_OUT_F32 ? 3 : 2;
-    const RouteWs w = route_ws(a.T, a.H, a.E, planes);
+    const int terms = a.dx_dtype == MOE_OUT_F32 ? 2 : 1;   // of dx's factors
+    const RouteWs w = route_ws(a.T, a.H, a.E, terms);
     const size_t ne = (size_t)a.E * a.H;
     if (a.T == 0) {
         if (a.dwr) MOE_LAUNCH("route_zero", route_zero, dim3(512), dim3(256), 0, st, a.dwr, ne);
@@ -881,15 +948,15 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st
         return hipGetLastError();
     }
     if (a.T <= kFewTokens) return launch_few(a, ws, st);
-    if (planes == 3)
-        launch_operands<3>(a, w, ws, st);
-    else
+    if (terms == 2)
         launch_operands<2>(a, w, ws, st);
+    else
+        launch_operands<1>(a, w, ws, st);
     if (a.dx) {
-        if (planes == 3)
-            launch_dx<3, float>(a, w, ws, st);
+        if (terms == 2)
+            launch_dx<2, float>(a, w, ws, st);
         else
-            launch_dx<2, Bf16>(a, w, ws, st);
+            launch_dx<1, Bf16>(a, w, ws, st);
     }
     float *part = reinterpret_cast<float *>(ws + w.dwp);
     if (a.dwr) {

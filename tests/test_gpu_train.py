@@ -392,12 +392,22 @@ class Route:
         wx, ww, wb = ot.route_backward(dz, np.where(keep[:, None], self.xv, 0), f64(self.wr), m)
         W, X, Z = np.abs(f64(self.wr)), np.abs(np.where(keep[:, None], self.xv, 0)), np.abs(dz)
         Ep = -(-E // 32) * 32
-        # dx: bf16 out takes two terms of each factor (2^-16 left of each, and
-        # lo lo), fp32 out three and six products; each addition of the fp32
-        # accumulation rounds once (2 U: a matrix core may truncate)
-        split, nprod = (3 * 2.0 ** -16, 3) if self.dx.dtype == B16 else (4 * 2.0 ** -24, 6)
-        b = err @ W + (split + 2 * U * nprod * Ep) * (Z @ W)
-        close(self.dx, wx, b + (UB if self.dx.dtype == B16 else U) * (np.abs(wx) + b))
+        # dx above 32 tokens: fp16 terms of factors scaled per row (dz) and
+        # column (Wr) to a largest magnitude of 2^14 or more.  A term leaves
+        # 2^-11 of the value, two leave 2^-22, and what is under half of fp16's
+        # least step, 2^-25, i.e. 2^-39 of the largest.  bf16 out: one term,
+        # |zw - z1 w1| <= (2 2^-11 + 2^-22) |z||w|.  fp32 out: hi hi + hi lo +
+        # lo hi: 2 2^-22 left of the factors and lo lo <= 2^-22.  Up to 32 tokens
+        # the products are fp32's.  The accumulation rounds once for each of
+        # nprod Ep additions (2 U: a matrix core may truncate).
+        one = self.dx.dtype == B16
+        split, nprod = (2.001 * 2.0 ** -11, 1) if one else (3 * 2.0 ** -22, 3)
+        floor = 2.0 ** -38 * (Z.max(1, keepdims=True) * W.sum(0) + Z.sum(1, keepdims=True) * W.max(0))
+        if T <= 32:
+            split, nprod, floor = U, 1, 0
+        b = err @ W + (split + 2 * U * nprod * (Ep + 32)) * (Z @ W) + floor
+        # and half the least step that the stored type has: 2^-133 (bf16), 2^-149 (fp32)
+        close(self.dx, wx, b + (UB if one else U) * (np.abs(wx) + b) + (2.0 ** -134 if one else 2.0 ** -150))
         n = 3 * (-(-T // 32) * 32) + 16
         close(self.dwr, ww, err.T @ X + (2.0 ** -24 + 2 * U * n + 2 * U) * (Z.T @ X))
         close(self.db, wb, err.sum(0) + (8 + T / 32 / 8 + 14) * U * Z.sum(0))
@@ -442,6 +452,43 @@ def test_route_backward_dropped_and_repeated_ids(renorm):
     c.ids[7] = -1
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("dxt", [B16, F32])
+def test_route_backward_magnitudes(dxt):
+    """Rows of dz and columns of Wr over many decades, within and between rows:
+    the scaling keeps every row's own precision."""
+    c = Route(90, 256, 72, 3, "x", True, dw=False, dxt=dxt)
+    g = torch.Generator().manual_seed(3)
+    c.dz *= 10.0 ** (torch.rand((90, 1), generator=g) * 40 - 30).cuda()
+    c.dz[:45] *= 10.0 ** -(torch.rand((45, 72), generator=g) * 9).cuda()
+    c.dz[3] = 0
+    c.wr *= 10.0 ** (torch.rand((1, 256), generator=g) * 20 - 15).cuda()
+    c.wr[:, :128] *= 10.0 ** -(torch.rand((72, 128), generator=g) * 9).cuda()
+    c.wr[:, 5] = 0
+    c.run()
+    c.check()
+
+
+def test_route_backward_nonfinite_rows():
+    """A non-finite entry makes its own row (or column) non-finite and no other."""
+    for dxt in (B16, F32):
+        c = Route(70, 256, 40, 3, "x", True, dw=False, dxt=dxt)
+        c.dz[4, 7] = float("inf")
+        c.dz[40, 0] = float("nan")
+        c.wr[9, 200] = float("-inf")
+        c.run()
+        torch.cuda.synchronize()
+        bad = ~torch.isfinite(c.dx)
+        want = torch.zeros_like(bad)
+        want[4] = want[40] = True
+        want[:, 200] = True
+        assert torch.equal(bad, want)
+        bad = ~torch.isfinite(c.dwr)
+        want = torch.zeros_like(bad)
+        want[7] = want[0] = True
+        assert torch.equal(bad, want)
+        assert not torch.isfinite(c.db[[0, 7]]).any() and torch.isfinite(c.db[1:7]).all()
 
 
 def test_route_backward_parts():
