@@ -214,12 +214,15 @@ __device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[
 }
 
 // 32 columns of Wr [E][H] as scaled units (32 hidden columns, 16 experts):
-// first the columns' maxima, then, from the cache, the values.
+// first the columns' maxima, then, from the cache, the values.  Group 2 b + o
+// holds the columns 64 b + o, 64 b + o + 2, ...: a lane of the product then has
+// two neighbouring columns, which it stores as one.
 template <int NP>
 __device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int32_t *__restrict__ hscale, int EC, int hg,
                          float *lds) {
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const float *col = a.wr + 32 * hg + (lane & 31);
+    const int h = 64 * (hg >> 1) + (hg & 1) + 2 * (lane & 31);
+    const float *col = a.wr + h;
     float m = 0.f;
 #pragma unroll 4
     for (int e = tid >> 5; e < a.E; e += 32) {
@@ -233,7 +236,7 @@ __device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int32
 #pragma unroll
     for (int r = 0; r < 32; ++r) m = fmaxf(m, lds[32 * r + (lane & 31)]);
     const int sc = scale_exponent(m);
-    if (tid < 32) hscale[32 * hg + tid] = sc;
+    if (tid < 32) hscale[h] = sc;
     for (int ec = wave; ec < EC; ec += 16) {
         float v[8];
 #pragma unroll
@@ -344,9 +347,47 @@ __device__ __forceinline__ V lds_unit(const uint8_t *p) {
     return *reinterpret_cast<const V *>(p + 16 * (threadIdx.x & 63));
 }
 
-// One linear copy of a unit into LDS by this wave.
-__device__ __forceinline__ void fill_unit(const uint8_t *src, uint8_t *dst) {
-    lds_fill<16>(buffer_rsrc(src, kUnit), 16 * (threadIdx.x & 63), dst);
+// The schedule of both products.  Eight waves, two per SIMD, in two groups
+// (waves 0..3 and 4..7: one of each per SIMD) that take turns: while one reads
+// its operands of a step from LDS into registers, the other runs its MFMAs.
+// With all waves in the same phase the reads and the MFMAs follow each other
+// (measured on dWr without any fills: 68 us of reads and MFMAs in turn, of
+// which 31 us are MFMAs).  Phases are separated by barriers; in step s
+//   even phase: everyone starts the fills of step s + 2 into the stage of step
+//               s - 1 (whose readers are done); group 0 reads step s, group 1
+//               runs the MFMAs of step s - 1;
+//   odd phase:  group 0 runs the MFMAs of step s, group 1 reads step s; at its
+//               end the fills of step s + 1 are awaited, those of s + 2 are not.
+// LDS operations are done at the end of every phase.  N: global operations
+// that this wave has issued after the fills it awaits.
+template <int N>
+__device__ __forceinline__ void odd_end() {
+    __builtin_amdgcn_sched_barrier(0);   // nothing changes its phase
+    fill_barrier<N>();
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void even_end() {
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();   // the fills stay in flight
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// For lambdas that are called from several places: a call would keep the
+// accumulators in memory.
+#define MOE_INLINE __attribute__((always_inline))
+
+// Wait until at most N of this wave's global operations are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_vmem_to() {
+    static_assert(N >= 0 && N <= 63, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
+
+// Unit i of the n consecutive units at src to dst + i units, by this wave.
+__device__ __forceinline__ void fill_unit(const uint8_t *src, int n, uint8_t *dst, int i) {
+    lds_fill<16>(buffer_rsrc(src, n * kUnit), i * kUnit + 16 * (threadIdx.x & 63), dst + i * kUnit);
 }
 
 // Tiles of dx in the order an XCD takes them: hidden tiles in groups of `hper`
@@ -364,11 +405,12 @@ struct DxTiles {
 
 // dx = dz Wr: 128 tokens x 256 hidden columns per tile, contraction over the
 // experts in steps of 64 (one term) or 32 (two), eight waves of 64 x 64.  MFMA
-// rows = hidden columns, columns = tokens: a lane ends with four consecutive
-// columns of one token.  One block per compute unit takes every 32nd tile of
-// its XCD's share and runs their steps as one sequence, so that the next
-// tile's operands are on their way while a tile is finished and stored.  LDS
-// is a ring of three 48 KB stages, filled two steps ahead.
+// rows = tokens, columns = hidden columns, the even ones of a wave's 64 in one
+// tile and the odd ones in the other: every store is whole rows of 64 columns.
+// One block per compute unit takes every 32nd tile of its XCD's share and runs
+// their steps as one sequence, so that the next tile's operands are on their
+// way while a tile is finished and stored.  LDS is a ring of three 48 KB
+// stages, filled two steps ahead.
 template <int NP, typename DX>
 __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp,
                                                 const int32_t *__restrict__ tscale, const int32_t *__restrict__ hscale,
@@ -391,7 +433,7 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
     // once everything is on its way; those fills land in a stage nobody reads)
     int ftile = first, fs = 0;
     const uint8_t *fa, *fb;
-    auto seek = [&](int tile) {
+    auto seek = [&](int tile) MOE_INLINE {
         int ht, tt;
         tiles.at(tile, ht, tt);
         const int hg = 8 * ht + wave < HG ? 8 * ht + wave : HG - 1;
@@ -400,11 +442,13 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
         fb = dza + ((size_t)tg * EC * NP + 2 * (wave & 1)) * kUnit;
     };
     seek(first);
-    auto fill = [&](uint8_t *st) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) fill_unit(fa + u * kUnit, st + (wave * 4 + u) * kUnit);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) fill_unit(fb + u * kUnit, st + kOpA + (wave * 2 + u) * kUnit);
+    auto fill_piece = [&](uint8_t *st, int u) MOE_INLINE {   // u in [0, kFills)
+        if (u < 4)
+            fill_unit(fa, 4, st + wave * 4 * kUnit, u);
+        else
+            fill_unit(fb, 2, st + kOpA + wave * 2 * kUnit, u - 4);
+    };
+    auto fill_next = [&]() MOE_INLINE {
         if (fs + 1 < S) {
             ++fs;
             fa += 4 * kUnit;
@@ -415,116 +459,177 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
             seek(ftile);
         }
     };
+    auto fill = [&](uint8_t *st) MOE_INLINE {
+#pragma unroll
+        for (int u = 0; u < kFills; ++u) fill_piece(st, u);
+        fill_next();
+    };
     const int wr = wave >> 1, wc = wave & 1;   // this wave's 64 hidden columns and 64 tokens
     f32x16 acc[2][2];
-    auto clear = [&]() {
+    f16x8 A[KC][2][NP], B[KC][2][NP];   // A: tokens, B: hidden columns
+    auto read = [&](const uint8_t *st) MOE_INLINE {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    };
-    clear();
-    int tile = first, s = 0;
-    auto store = [&]() {
-        int ht, tt;
-        tiles.at(tile, ht, tt);
-        int4 hs[2][4];   // the scales of this lane's columns (past H: of the last ones, not stored)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
-                hs[i][q] = *reinterpret_cast<const int4 *>(hscale + (h < H ? h : H - 4));
-            }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = kTileT * tt + 64 * wc + 32 * j + (lane & 31);
-            const int ts = tscale[t < T ? t : T - 1];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int h = kTileH * ht + 64 * wr + 32 * i + 8 * q + 4 * (lane >> 5);
-                    const float v0 = ldexpf(acc[i][j][4 * q], -ts - hs[i][q].x);
-                    const float v1 = ldexpf(acc[i][j][4 * q + 1], -ts - hs[i][q].y);
-                    const float v2 = ldexpf(acc[i][j][4 * q + 2], -ts - hs[i][q].z);
-                    const float v3 = ldexpf(acc[i][j][4 * q + 3], -ts - hs[i][q].w);
-                    const size_t at = (size_t)t * H + h;
-                    if (t < T && h < H) {
-                        if constexpr (__is_same(DX, float))
-                            *reinterpret_cast<float4 *>(static_cast<float *>(dx) + at) = make_float4(v0, v1, v2, v3);
-                        else
-                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dx) + at) =
-                                make_uint2(bf16x2_bits(v0, v1), bf16x2_bits(v2, v3));
-                    }
-                }
-        }
-    };
-    // One step: the stage's fills are in once at most those of the next step
-    // are outstanding (stores in between only make the wait longer); after the
-    // barrier everyone's are, and everyone is done with the stage of the step
-    // before, which is filled next.
-    auto step = [&](const uint8_t *cur, uint8_t *next) {
-        fill_barrier<kFills>();
-        fill(next);
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-            f16x8 A[2][NP], B[2][NP];
+        for (int c = 0; c < KC; ++c)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    A[i][p] = lds_unit<f16x8>(cur + ((2 * wr + i) * 4 + c * NP + p) * kUnit);
-                    B[i][p] = lds_unit<f16x8>(cur + kOpA + ((2 * wc + i) * 4 + c * NP + p) * kUnit);
+                    A[c][i][p] = lds_unit<f16x8>(st + kOpA + ((2 * wc + i) * 4 + c * NP + p) * kUnit);
+                    B[c][i][p] = lds_unit<f16x8>(st + ((2 * wr + i) * 4 + c * NP + p) * kUnit);
                 }
+    };
+    int tile = first, s = 0;   // of the next products
+    constexpr int kSize = __is_same(DX, float) ? 4 : 2;
+    const int half = lane >> 5;
+    // scales of a tile, loaded when the one before it is done: this lane's two
+    // columns, and token `lane` of the wave's 64
+    int2 hs;
+    int ts;
+    auto scales = [&](int idx) MOE_INLINE {
+        int ht, tt;
+        tiles.at(idx, ht, tt);
+        const int h = kTileH * ht + 64 * wr + 2 * (lane & 31), t = kTileT * tt + 64 * wc + lane;
+        hs = *reinterpret_cast<const int2 *>(hscale + (h < H ? h : H - 2));
+        ts = tscale[t < T ? t : T - 1];
+    };
+    scales(first);
+    // The finished tile: scaled back and stored, two columns of a row at once.
+    // Rows past T are outside the buffer, lanes past H get an offset that is.
+    auto store = [&]() MOE_INLINE {
+        int ht, tt;
+        tiles.at(tile, ht, tt);
+        const int h = kTileH * ht + 64 * wr + 2 * (lane & 31);
+        const int t0 = kTileT * tt + 64 * wc;
+        const int rows = T - t0 < 64 ? T - t0 : 64;
+        const __amdgpu_buffer_rsrc_t out = buffer_rsrc(static_cast<uint8_t *>(dx) + (size_t)(rows > 0 ? t0 : 0) * H * kSize,
+                                                       rows > 0 ? (uint32_t)rows * H * kSize : 0u);
+        const uint32_t lane_off = h < H ? ((uint32_t)(4 * half) * H + h) * kSize : 0x80000000u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 32 * i + 8 * q + r;   // + 4 in the upper half
+                    const int lo = __builtin_amdgcn_readlane(ts, row), hi = __builtin_amdgcn_readlane(ts, row + 4);
+                    const int tr = half ? hi : lo;
+                    const float v0 = ldexpf(acc[i][0][4 * q + r], -tr - hs.x);
+                    const float v1 = ldexpf(acc[i][1][4 * q + r], -tr - hs.y);
+                    const uint32_t off = lane_off + (uint32_t)row * H * kSize;
+                    if constexpr (__is_same(DX, float)) {
+                        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                        const u32x2 v = {__float_as_uint(v0), __float_as_uint(v1)};
+                        __builtin_amdgcn_raw_buffer_store_b64(v, out, off, 0, 0);
+                    } else {
+                        __builtin_amdgcn_raw_buffer_store_b32(bf16x2_bits(v0, v1), out, off, 0, 0);
+                    }
+                }
+    };
+    // Products of the step read last, with the fills of `next` between them
+    // when it is given (a wave issues them while its MFMAs run); true when
+    // they finished a tile.
+    auto products = [&](uint8_t *next) MOE_INLINE {
+        if (s == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+        }
+        int u = 0;
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
 #pragma unroll
             for (int p = 0; p < NP; ++p)
 #pragma unroll
-                for (int q = 0; q < NP - p; ++q)
+                for (int q = 0; q < NP - p; ++q) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i][p], B[j][q], acc[i][j], 0, 0, 0);
-        }
-        if (++s == S) {
-            store();
-            clear();
-            s = 0;
-            tile += slots;
-        }
-        return tile < last;
+                            acc[i][j] =
+                                __builtin_amdgcn_mfma_f32_32x32x16_f16(A[c][i][p], B[c][j][q], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (next) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (u < kFills) fill_piece(next, u++);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        if (next) fill_next();
+        if (++s < S) return false;
+        // the fills awaited at the end of the odd phase, before stores follow them
+        wait_vmem_to<kFills>();
+        store();
+        s = 0;
+        tile += slots;
+        scales(tile < last ? tile : first);
+        return true;
+    };
+    const int steps = S * ((last - first + slots - 1) / slots);
+    auto wait = [&](bool stored) MOE_INLINE {
+        if (stored)
+            even_end();
+        else
+            odd_end<kFills>();
+    };
+    auto step0 = [&](const uint8_t *cur, uint8_t *next) MOE_INLINE {   // group 0
+        fill(next);
+        read(cur);
+        even_end();
+        wait(products(nullptr));
+    };
+    auto step1 = [&](const uint8_t *cur, uint8_t *next) MOE_INLINE {   // group 1
+        const bool stored = products(next);
+        even_end();
+        read(cur);
+        wait(stored);
     };
     fill(st0);
     fill(st1);
-    while (step(st0, st2) && step(st1, st0) && step(st2, st1)) {}
+    odd_end<kFills>();
+    if (wave < 4) {
+        for (int g = 0; g < steps; g += 3) {
+            step0(st0, st2);
+            if (g + 1 < steps) step0(st1, st0);
+            if (g + 2 < steps) step0(st2, st1);
+        }
+    } else {
+        fill(st2);   // the first step has no products before it
+        even_end();
+        read(st0);
+        wait(false);
+        for (int g = 1; g < steps; g += 3) {
+            step1(st1, st0);
+            if (g + 1 < steps) step1(st2, st1);
+            if (g + 2 < steps) step1(st0, st2);
+        }
+        products(nullptr);
+    }
 }
 
 // ----------------------------------- dWr -----------------------------------
 // Tokens of one thread's piece of a step: two hidden columns x eight tokens,
-// as two bf16 per dword (x) or two codes and their scale (checkpoint).  Every
-// row is a buffer of its own with the row's length, or none for a row that
-// takes no part (past the end, or masked): such rows and columns past H read
-// as zeros, whatever is stored there.
+// as two bf16 per dword (x) or two codes and their scale (checkpoint).  The
+// eight rows are one buffer; a row that takes no part (past the end, or
+// masked) gets an offset outside it and reads as zeros, whatever is stored.
+// (Columns past H read some value; their results are not stored.)
 template <bool MX>
 struct XPiece {
     uint32_t v[8];
     uint32_t s[MX ? 8 : 1];
-    // rows t0 .. t0 + 7 (uniform), bit i of `valid` for row t0 + i; column h
-    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, int h) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t in = (valid >> i) & 1u;
-            const size_t row = (size_t)(t0 + i) * a.H;
-            if constexpr (MX) {
-                v[i] = __builtin_amdgcn_raw_buffer_load_b16(buffer_rsrc(a.codes + row, in ? a.H : 0), h, 0, 0);
-                s[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(a.scales + (row >> 5), in ? a.H >> 5 : 0),
-                                                           h >> 5, 0, 0);
-            } else {
-                v[i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(a.x + row, in ? 2 * a.H : 0), 2 * h, 0, 0);
-            }
+    // row t0 + i (t0 uniform), bit i of `valid` for it; column h
+    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, int h, int i) {
+        const bool in = (valid >> i) & 1u;
+        const size_t row = (size_t)t0 * a.H;
+        const uint32_t at = in ? (uint32_t)i * a.H + h : 0x40000000u;
+        if constexpr (MX) {
+            v[i] = __builtin_amdgcn_raw_buffer_load_b16(buffer_rsrc(a.codes + row, 8 * a.H), at, 0, 0);
+            s[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(a.scales + (row >> 5), a.H >> 2), at >> 5, 0, 0);
+        } else {
+            v[i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(a.x + row, 16 * a.H), 2 * at, 0, 0);
         }
     }
     // the eight tokens of column h (lo) and h + 1 (hi) as 16-byte pieces
@@ -587,10 +692,8 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     // dz units of this wave: expert group wave / 2 of the tile, chunk wave % 2
     const int eg = 4 * et + (wave >> 1) < EG ? 4 * et + (wave >> 1) : EG - 1;
-    auto fill_a = [&](uint8_t *st, int s) {
-        const uint8_t *src = dzt + ((size_t)(2 * s + (wave & 1)) * EG + eg) * 3 * kUnit;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) fill_unit(src + p * kUnit, st + (wave * 3 + p) * kUnit);
+    auto fill_a = [&](uint8_t *st, int s, int p) MOE_INLINE {
+        fill_unit(dzt + ((size_t)(2 * s + (wave & 1)) * EG + eg) * 3 * kUnit, 3, st + wave * 3 * kUnit, p);
     };
     // x piece of this thread: hidden columns 128 (wave % 2) + 2 lane, + 1 of
     // the tile, tokens 8 (wave / 2) .. +7 of the step
@@ -599,7 +702,7 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
     const int xunit = ((4 * (wave & 1) + (lane >> 4)) * 2 + (oct >> 1)) * kUnit;
     const int slot = ((2 * lane) & 31) + 32 * (oct & 1);
     const int xlo = kA + xunit + x_slot(slot), xhi = kA + xunit + x_slot(slot + 1);
-    auto put_x = [&](uint8_t *st, XPiece<MX> &x) {
+    auto put_x = [&](uint8_t *st, XPiece<MX> &x) MOE_INLINE {
         uint4 lo, hi;
         x.pieces(lo, hi);
         *reinterpret_cast<uint4 *>(st + xlo) = lo;
@@ -613,54 +716,108 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    uint32_t ok2 = 0;   // the tokens that count in the step whose x rows are loaded next
-    // Step s: computes from `cur`, fills `nn` (s + 2), writes x of s + 1 to
-    // `next`.  Steps past the end load the last one again, into a stage that
-    // nobody reads, so that the counts below hold to the end.
-    auto step = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn, int s) {
-        // all but the newest step's loads are done: the dz units of step s;
-        // the wait on LDS covers its x rows.  After the barrier that holds for
-        // every wave, and every wave is done with step s - 1, whose stage nn is
-        fill_barrier<kLoads>();
-        const int n = s + 2 < s1 ? s + 2 : s1 - 1;
-        fill_a(nn, n);
-        xnn.load(a, kStepK * n + 8 * oct, ok2 >> (8 * oct), h);
-        ok2 = valid[s + 3 < s1 ? s + 3 : s1 - 1];
+    // bit i: token 8 oct + i of step s takes part
+    auto tokens = [&](int s) MOE_INLINE {
+        if (a.mask) return valid[s] >> (8 * oct);
+        const int n = a.T - (kStepK * s + 8 * oct);
+        return n >= 8 ? 0xffu : n > 0 ? (1u << n) - 1u : 0u;
+    };
+    uint32_t ok2 = 0;   // of the step whose x rows are loaded next
+    // Piece k of 6 of the start of step s + 2: its dz units into `nn`, its x
+    // rows into registers.  Steps past the end load the last one again, into a
+    // stage that nobody reads, so that the counts of odd_end hold to the end.
+    auto issue = [&](uint8_t *nn, XPiece<MX> &xnn, int s, int k) MOE_INLINE {
+        const int n = s + 2 < s1 ? s + 2 : s1 - 1, t0 = kStepK * n + 8 * oct;
+        if (k < 3) fill_a(nn, n, k);
+        if (k < 4) {
+            xnn.load(a, t0, ok2, h, 2 * k);
+            xnn.load(a, t0, ok2, h, 2 * k + 1);
+        }
+        if (k == 5) ok2 = tokens(s + 3 < s1 ? s + 3 : s1 - 1);
+    };
+    auto issue_all = [&](uint8_t *nn, XPiece<MX> &xnn, int s) MOE_INLINE {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            bf16x8 A[2][3], B[2];
+        for (int k = 0; k < 6; ++k) issue(nn, xnn, s, k);
+    };
+    bf16x8 A[2][2][3], B[2][2];
+    auto read = [&](const uint8_t *st) MOE_INLINE {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int p = 0; p < 3; ++p) A[i][p] = lds_unit<bf16x8>(cur + (((2 * wr + i) * 2 + c) * 3 + p) * kUnit);
-                B[i] = *reinterpret_cast<const bf16x8 *>(cur + kA + ((2 * wc + i) * 2 + c) * kUnit + x_slot(lane));
+                for (int p = 0; p < 3; ++p)
+                    A[c][i][p] = lds_unit<bf16x8>(st + (((2 * wr + i) * 2 + c) * 3 + p) * kUnit);
+                B[c][i] = *reinterpret_cast<const bf16x8 *>(st + kA + ((2 * wc + i) * 2 + c) * kUnit + x_slot(lane));
             }
+    };
+    // Products in six groups of four, with work(k) after group k (a wave
+    // issues it while its MFMAs run).
+    auto products = [&](auto &&work) MOE_INLINE {
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[i][p], B[j], acc[i][j]);
-        }
+                    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[c][i][p], B[c][j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+                work(3 * c + p);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    };
+    // Step s from `cur`; x of step s + 1 goes to `next` in the odd phase.
+    auto step0 = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn,
+                     int s) MOE_INLINE {
+        read(cur);
+        issue_all(nn, xnn, s);
+        even_end();
+        products([&](int k) MOE_INLINE {
+            if (k == 1) put_x(next, xnext);
+        });
+        odd_end<kLoads>();
+    };
+    auto step1 = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn,
+                     int s) MOE_INLINE {
+        products([&](int k) MOE_INLINE { issue(nn, xnn, s, k); });
+        even_end();
+        read(cur);
         put_x(next, xnext);
+        odd_end<kLoads>();
     };
     if (s0 < s1) {
         XPiece<MX> x0, x1;
-        const int n = s0 + 1 < s1 ? s0 + 1 : s1 - 1;
-        const uint32_t ok0 = valid[s0], ok1 = valid[n];
-        ok2 = valid[s0 + 2 < s1 ? s0 + 2 : s1 - 1];
-        fill_a(st0, s0);
-        x0.load(a, kStepK * s0 + 8 * oct, ok0 >> (8 * oct), h);
-        fill_a(st1, n);
-        x1.load(a, kStepK * n + 8 * oct, ok1 >> (8 * oct), h);
+        ok2 = tokens(s0);
+        issue_all(st0, x0, s0 - 2);
+        issue_all(st1, x1, s0 - 1);
         put_x(st0, x0);
-        for (int s = s0; s < s1; s += 6) {   // one exit: with one per step every step's tile would be kept apart
-            step(st0, st1, st2, x1, x0, s);
-            if (s + 1 < s1) step(st1, st2, st0, x0, x1, s + 1);
-            if (s + 2 < s1) step(st2, st0, st1, x1, x0, s + 2);
-            if (s + 3 < s1) step(st0, st1, st2, x0, x1, s + 3);
-            if (s + 4 < s1) step(st1, st2, st0, x1, x0, s + 4);
-            if (s + 5 < s1) step(st2, st0, st1, x0, x1, s + 5);
+        odd_end<kLoads>();
+        // one exit per loop: with one per step every step's tile would be kept apart
+        if (wave < 4) {
+            for (int s = s0; s < s1; s += 6) {
+                step0(st0, st1, st2, x1, x0, s);
+                if (s + 1 < s1) step0(st1, st2, st0, x0, x1, s + 1);
+                if (s + 2 < s1) step0(st2, st0, st1, x1, x0, s + 2);
+                if (s + 3 < s1) step0(st0, st1, st2, x0, x1, s + 3);
+                if (s + 4 < s1) step0(st1, st2, st0, x1, x0, s + 4);
+                if (s + 5 < s1) step0(st2, st0, st1, x0, x1, s + 5);
+            }
+        } else {
+            issue_all(st2, x0, s0);   // the first step has no products before it
+            even_end();
+            read(st0);
+            put_x(st1, x1);
+            odd_end<kLoads>();
+            for (int s = s0 + 1; s < s1; s += 6) {
+                step1(st1, st2, st0, x0, x1, s);
+                if (s + 1 < s1) step1(st2, st0, st1, x1, x0, s + 1);
+                if (s + 2 < s1) step1(st0, st1, st2, x0, x1, s + 2);
+                if (s + 3 < s1) step1(st1, st2, st0, x1, x0, s + 3);
+                if (s + 4 < s1) step1(st2, st0, st1, x0, x1, s + 4);
+                if (s + 5 < s1) step1(st0, st1, st2, x1, x0, s + 5);
+            }
+            products([&](int) MOE_INLINE {});
         }
     }
     float *const dst = out + (splits > 1 ? (size_t)sp * E * H : 0);
