@@ -353,11 +353,14 @@ __device__ __forceinline__ V lds_unit(const uint8_t *p) {
 // With all waves in the same phase the reads and the MFMAs follow each other
 // (measured on dWr without any fills: 68 us of reads and MFMAs in turn, of
 // which 31 us are MFMAs).  Phases are separated by barriers; in step s
-//   even phase: everyone starts the fills of step s + 2 into the stage of step
-//               s - 1 (whose readers are done); group 0 reads step s, group 1
-//               runs the MFMAs of step s - 1;
-//   odd phase:  group 0 runs the MFMAs of step s, group 1 reads step s; at its
-//               end the fills of step s + 1 are awaited, those of s + 2 are not.
+//   even phase: group 0 reads step s and starts its fills of step s + 2 into the
+//               stage of step s - 1 (whose readers are done); group 1 runs the
+//               MFMAs of step s - 1;
+//   odd phase:  group 0 runs the MFMAs of step s; group 1 reads step s and starts
+//               its fills of step s + 2; at its end the fills of step s + 1 are
+//               awaited, those of s + 2 are not.
+// (A wave that has loads between its MFMAs waits for the address unit that the
+// other group's loads keep busy.)
 // LDS operations are done at the end of every phase.  N: global operations
 // that this wave has issued after the fills it awaits.
 template <int N>
@@ -442,13 +445,11 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
         fb = dza + ((size_t)tg * EC * NP + 2 * (wave & 1)) * kUnit;
     };
     seek(first);
-    auto fill_piece = [&](uint8_t *st, int u) MOE_INLINE {   // u in [0, kFills)
-        if (u < 4)
-            fill_unit(fa, 4, st + wave * 4 * kUnit, u);
-        else
-            fill_unit(fb, 2, st + kOpA + wave * 2 * kUnit, u - 4);
-    };
-    auto fill_next = [&]() MOE_INLINE {
+    auto fill = [&](uint8_t *st) MOE_INLINE {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) fill_unit(fa, 4, st + wave * 4 * kUnit, u);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) fill_unit(fb, 2, st + kOpA + wave * 2 * kUnit, u);
         if (fs + 1 < S) {
             ++fs;
             fa += 4 * kUnit;
@@ -458,11 +459,6 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
             fs = 0;
             seek(ftile);
         }
-    };
-    auto fill = [&](uint8_t *st) MOE_INLINE {
-#pragma unroll
-        for (int u = 0; u < kFills; ++u) fill_piece(st, u);
-        fill_next();
     };
     const int wr = wave >> 1, wc = wave & 1;   // this wave's 64 hidden columns and 64 tokens
     f32x16 acc[2][2];
@@ -525,10 +521,9 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
                     }
                 }
     };
-    // Products of the step read last, with the fills of `next` between them
-    // when it is given (a wave issues them while its MFMAs run); true when
-    // they finished a tile.
-    auto products = [&](uint8_t *next) MOE_INLINE {
+    // Products of the step read last; true when they finished a tile, and
+    // (group 0) the fills due at the end of the phase have been awaited.
+    auto products = [&]() MOE_INLINE {
         if (s == 0) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -537,31 +532,20 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
 #pragma unroll
                     for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
         }
-        int u = 0;
 #pragma unroll
         for (int c = 0; c < KC; ++c)
 #pragma unroll
             for (int p = 0; p < NP; ++p)
 #pragma unroll
-                for (int q = 0; q < NP - p; ++q) {
+                for (int q = 0; q < NP - p; ++q)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             acc[i][j] =
                                 __builtin_amdgcn_mfma_f32_32x32x16_f16(A[c][i][p], B[c][j][q], acc[i][j], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (next) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (u < kFills) fill_piece(next, u++);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-        if (next) fill_next();
         if (++s < S) return false;
-        // the fills awaited at the end of the odd phase, before stores follow them
-        wait_vmem_to<kFills>();
+        if (wave < 4) wait_vmem_to<kFills>();   // before stores follow them
         store();
         s = 0;
         tile += slots;
@@ -575,38 +559,40 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
         else
             odd_end<kFills>();
     };
-    auto step0 = [&](const uint8_t *cur, uint8_t *next) MOE_INLINE {   // group 0
-        fill(next);
-        read(cur);
-        even_end();
-        wait(products(nullptr));
-    };
-    auto step1 = [&](const uint8_t *cur, uint8_t *next) MOE_INLINE {   // group 1
-        const bool stored = products(next);
-        even_end();
-        read(cur);
-        wait(stored);
-    };
     fill(st0);
     fill(st1);
     odd_end<kFills>();
     if (wave < 4) {
+        auto step = [&](const uint8_t *cur, uint8_t *next) MOE_INLINE {
+            read(cur);
+            fill(next);
+            even_end();
+            wait(products());
+        };
         for (int g = 0; g < steps; g += 3) {
-            step0(st0, st2);
-            if (g + 1 < steps) step0(st1, st0);
-            if (g + 2 < steps) step0(st2, st1);
+            step(st0, st2);
+            if (g + 1 < steps) step(st1, st0);
+            if (g + 2 < steps) step(st2, st1);
         }
     } else {
-        fill(st2);   // the first step has no products before it
-        even_end();
-        read(st0);
-        wait(false);
-        for (int g = 1; g < steps; g += 3) {
-            step1(st1, st0);
-            if (g + 1 < steps) step1(st2, st1);
-            if (g + 2 < steps) step1(st0, st2);
+        auto step = [&](const uint8_t *cur, uint8_t *next) MOE_INLINE {   // after the even phase's end
+            read(cur);
+            fill(next);
+            odd_end<kFills>();
+            products();
+        };
+        for (int g = 0; g < steps; g += 3) {
+            even_end();
+            step(st0, st2);
+            if (g + 1 < steps) {
+                even_end();
+                step(st1, st0);
+            }
+            if (g + 2 < steps) {
+                even_end();
+                step(st2, st1);
+            }
         }
-        products(nullptr);
     }
 }
 
@@ -614,17 +600,18 @@ __global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza,
 // Tokens of one thread's piece of a step: two hidden columns x eight tokens,
 // as two bf16 per dword (x) or two codes and their scale (checkpoint).  The
 // eight rows are one buffer; a row that takes no part (past the end, or
-// masked) gets an offset outside it and reads as zeros, whatever is stored.
-// (Columns past H read some value; their results are not stored.)
+// masked) and a column past H get an offset outside it and read as zeros,
+// whatever is stored.
+constexpr uint32_t kOutside = 0x40000000u;   // elements; eight rows have at most 2^19
 template <bool MX>
 struct XPiece {
     uint32_t v[8];
     uint32_t s[MX ? 8 : 1];
-    // row t0 + i (t0 uniform), bit i of `valid` for it; column h
-    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, int h, int i) {
+    // row t0 + i (t0 uniform), bit i of `valid` for it; column h (kOutside: none)
+    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, uint32_t h, int i) {
         const bool in = (valid >> i) & 1u;
         const size_t row = (size_t)t0 * a.H;
-        const uint32_t at = in ? (uint32_t)i * a.H + h : 0x40000000u;
+        const uint32_t at = in ? (uint32_t)i * a.H + h : kOutside;
         if constexpr (MX) {
             v[i] = __builtin_amdgcn_raw_buffer_load_b16(buffer_rsrc(a.codes + row, 8 * a.H), at, 0, 0);
             s[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(a.scales + (row >> 5), a.H >> 2), at >> 5, 0, 0);
@@ -692,12 +679,10 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     // dz units of this wave: expert group wave / 2 of the tile, chunk wave % 2
     const int eg = 4 * et + (wave >> 1) < EG ? 4 * et + (wave >> 1) : EG - 1;
-    auto fill_a = [&](uint8_t *st, int s, int p) MOE_INLINE {
-        fill_unit(dzt + ((size_t)(2 * s + (wave & 1)) * EG + eg) * 3 * kUnit, 3, st + wave * 3 * kUnit, p);
-    };
     // x piece of this thread: hidden columns 128 (wave % 2) + 2 lane, + 1 of
     // the tile, tokens 8 (wave / 2) .. +7 of the step
-    const int h = kTileH * ht + 128 * (wave & 1) + 2 * lane;
+    const int hx = kTileH * ht + 128 * (wave & 1) + 2 * lane;
+    const uint32_t h = hx < H ? hx : kOutside;
     const int oct = wave >> 1;
     const int xunit = ((4 * (wave & 1) + (lane >> 4)) * 2 + (oct >> 1)) * kUnit;
     const int slot = ((2 * lane) & 31) + 32 * (oct & 1);
@@ -722,22 +707,19 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
         const int n = a.T - (kStepK * s + 8 * oct);
         return n >= 8 ? 0xffu : n > 0 ? (1u << n) - 1u : 0u;
     };
-    uint32_t ok2 = 0;   // of the step whose x rows are loaded next
-    // Piece k of 6 of the start of step s + 2: its dz units into `nn`, its x
-    // rows into registers.  Steps past the end load the last one again, into a
-    // stage that nobody reads, so that the counts of odd_end hold to the end.
-    auto issue = [&](uint8_t *nn, XPiece<MX> &xnn, int s, int k) MOE_INLINE {
-        const int n = s + 2 < s1 ? s + 2 : s1 - 1, t0 = kStepK * n + 8 * oct;
-        if (k < 3) fill_a(nn, n, k);
-        if (k < 4) {
-            xnn.load(a, t0, ok2, h, 2 * k);
-            xnn.load(a, t0, ok2, h, 2 * k + 1);
-        }
-        if (k == 5) ok2 = tokens(s + 3 < s1 ? s + 3 : s1 - 1);
-    };
-    auto issue_all = [&](uint8_t *nn, XPiece<MX> &xnn, int s) MOE_INLINE {
+    // Steps past the end load the last one again, into a stage (or registers)
+    // that nobody reads, so that the counts of odd_end hold to the end.
+    auto load_x = [&](XPiece<MX> &x, int s) MOE_INLINE {
+        const int n = s < s1 ? s : s1 - 1;
+        const uint32_t ok = tokens(n);
 #pragma unroll
-        for (int k = 0; k < 6; ++k) issue(nn, xnn, s, k);
+        for (int i = 0; i < 8; ++i) x.load(a, kStepK * n + 8 * oct, ok, h, i);
+    };
+    auto fill_a = [&](uint8_t *st, int s) MOE_INLINE {
+        const int n = s < s1 ? s : s1 - 1;
+        const uint8_t *src = dzt + ((size_t)(2 * n + (wave & 1)) * EG + eg) * 3 * kUnit;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) fill_unit(src, 3, st + wave * 3 * kUnit, p);
     };
     bf16x8 A[2][2][3], B[2][2];
     auto read = [&](const uint8_t *st) MOE_INLINE {
@@ -751,73 +733,67 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
                 B[c][i] = *reinterpret_cast<const bf16x8 *>(st + kA + ((2 * wc + i) * 2 + c) * kUnit + x_slot(lane));
             }
     };
-    // Products in six groups of four, with work(k) after group k (a wave
-    // issues it while its MFMAs run).
-    auto products = [&](auto &&work) MOE_INLINE {
+    auto products = [&](int c) MOE_INLINE {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int p = 0; p < 3; ++p)
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[c][i][p], B[c][j], acc[i][j]);
-                __builtin_amdgcn_sched_barrier(0);
-                work(3 * c + p);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-    };
-    // Step s from `cur`; x of step s + 1 goes to `next` in the odd phase.
-    auto step0 = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn,
-                     int s) MOE_INLINE {
-        read(cur);
-        issue_all(nn, xnn, s);
-        even_end();
-        products([&](int k) MOE_INLINE {
-            if (k == 1) put_x(next, xnext);
-        });
-        odd_end<kLoads>();
-    };
-    auto step1 = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn,
-                     int s) MOE_INLINE {
-        products([&](int k) MOE_INLINE { issue(nn, xnn, s, k); });
-        even_end();
-        read(cur);
-        put_x(next, xnext);
-        odd_end<kLoads>();
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(A[c][i][p], B[c][j], acc[i][j]);
     };
     if (s0 < s1) {
         XPiece<MX> x0, x1;
-        ok2 = tokens(s0);
-        issue_all(st0, x0, s0 - 2);
-        issue_all(st1, x1, s0 - 1);
+        fill_a(st0, s0);
+        load_x(x0, s0);
+        fill_a(st1, s0 + 1);
+        load_x(x1, s0 + 1);
         put_x(st0, x0);
-        odd_end<kLoads>();
-        // one exit per loop: with one per step every step's tile would be kept apart
         if (wave < 4) {
+            odd_end<kLoads>();
+            // x rows of step s + 2 in the even phase, to LDS (s + 1) in the odd one
+            auto step = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &xnext, XPiece<MX> &xnn,
+                            int s) MOE_INLINE {
+                read(cur);
+                fill_a(nn, s + 2);
+                load_x(xnn, s + 2);
+                even_end();
+                products(0);
+                put_x(next, xnext);
+                products(1);
+                odd_end<kLoads>();
+            };
+            // one exit per loop: with one per step every step's tile would be kept apart
             for (int s = s0; s < s1; s += 6) {
-                step0(st0, st1, st2, x1, x0, s);
-                if (s + 1 < s1) step0(st1, st2, st0, x0, x1, s + 1);
-                if (s + 2 < s1) step0(st2, st0, st1, x1, x0, s + 2);
-                if (s + 3 < s1) step0(st0, st1, st2, x0, x1, s + 3);
-                if (s + 4 < s1) step0(st1, st2, st0, x1, x0, s + 4);
-                if (s + 5 < s1) step0(st2, st0, st1, x0, x1, s + 5);
+                step(st0, st1, st2, x1, x0, s);
+                if (s + 1 < s1) step(st1, st2, st0, x0, x1, s + 1);
+                if (s + 2 < s1) step(st2, st0, st1, x1, x0, s + 2);
+                if (s + 3 < s1) step(st0, st1, st2, x0, x1, s + 3);
+                if (s + 4 < s1) step(st1, st2, st0, x1, x0, s + 4);
+                if (s + 5 < s1) step(st2, st0, st1, x0, x1, s + 5);
             }
         } else {
-            issue_all(st2, x0, s0);   // the first step has no products before it
-            even_end();
-            read(st0);
-            put_x(st1, x1);
-            odd_end<kLoads>();
-            for (int s = s0 + 1; s < s1; s += 6) {
-                step1(st1, st2, st0, x0, x1, s);
-                if (s + 1 < s1) step1(st2, st0, st1, x1, x0, s + 1);
-                if (s + 2 < s1) step1(st0, st1, st2, x0, x1, s + 2);
-                if (s + 3 < s1) step1(st1, st2, st0, x1, x0, s + 3);
-                if (s + 4 < s1) step1(st2, st0, st1, x0, x1, s + 4);
-                if (s + 5 < s1) step1(st0, st1, st2, x1, x0, s + 5);
+            load_x(x0, s0 + 2);
+            odd_end<2 * kLoads - 3>();   // newer than st0's fills: st1's and two steps of x
+            // x rows of step s + 1 to LDS and those of s + 3 into their
+            // registers, both in the odd phase
+            auto step = [&](const uint8_t *cur, uint8_t *next, uint8_t *nn, XPiece<MX> &x, int s) MOE_INLINE {
+                even_end();
+                read(cur);
+                put_x(next, x);
+                fill_a(nn, s + 2);
+                load_x(x, s + 3);
+                odd_end<kLoads>();
+                products(0);
+                products(1);
+            };
+            for (int s = s0; s < s1; s += 6) {
+                step(st0, st1, st2, x1, s);
+                if (s + 1 < s1) step(st1, st2, st0, x0, s + 1);
+                if (s + 2 < s1) step(st2, st0, st1, x1, s + 2);
+                if (s + 3 < s1) step(st0, st1, st2, x0, s + 3);
+                if (s + 4 < s1) step(st1, st2, st0, x1, s + 4);
+                if (s + 5 < s1) step(st2, st0, st1, x0, s + 5);
             }
-            products([&](int) MOE_INLINE {});
         }
     }
     float *const dst = out + (splits > 1 ? (size_t)sp * E * H : 0);
