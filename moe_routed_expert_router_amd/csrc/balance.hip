@@ -87,12 +87,20 @@ __device__ __forceinline__ void load_row(const float *zr, int E, float (&z)[NPL]
     }
 }
 
+// sum_e (counts / N) P of a group is at most k <= 32, of 2^15 groups 2^20: with
+// 42 fractional bits the sum stays below 2^62, and a block's part is off by
+// at most 2^-43.
+constexpr int kDotBits = 42;
+
 struct BalanceWs {
     float *psum;        // [items][E]
     int32_t *csum;      // [items][E]
     int32_t *nsum;      // [items]
-    double *dot;        // [S][column tiles]
-    uint32_t *done;     // finished reduction blocks
+    // running sums of the reduction's blocks, zero at its start: the loss in
+    // units of 2^-kDotBits (integers: any order gives the same sum), whether a
+    // part was NaN, groups with tokens, finished blocks
+    unsigned long long *dot;
+    uint32_t *nan, *live, *done;
     static size_t layout(int items, int E, int S, char *ws, BalanceWs *o) {
         size_t at = 0;
         auto take = [&](size_t n) {
@@ -104,8 +112,11 @@ struct BalanceWs {
         w.psum = reinterpret_cast<float *>(take((size_t)items * E * 4));
         w.csum = reinterpret_cast<int32_t *>(take((size_t)items * E * 4));
         w.nsum = reinterpret_cast<int32_t *>(take((size_t)items * 4));
-        w.dot = reinterpret_cast<double *>(take((size_t)S * ((E + 63) / 64) * 8));
-        w.done = reinterpret_cast<uint32_t *>(take(4));
+        char *const c = take(24);
+        w.dot = reinterpret_cast<unsigned long long *>(c);
+        w.nan = reinterpret_cast<uint32_t *>(c + 8);
+        w.live = reinterpret_cast<uint32_t *>(c + 12);
+        w.done = reinterpret_cast<uint32_t *>(c + 16);
         if (o) *o = w;
         return at;
     }
@@ -140,7 +151,10 @@ __global__ __launch_bounds__(kBalThreads) void balance_sums(BalanceArgs a, int R
     const int item = blockIdx.x;
     int t0 = 0, t1 = a.T;
     if constexpr (!ONE) {
-        if (item == 0 && tid == 0) *w.done = 0;   // read only by the next launch
+        if (item == 0 && tid == 0) {   // used only by the next launch
+            *w.dot = 0;
+            *w.nan = *w.live = *w.done = 0;
+        }
         const auto key = [&](int g) { return bound_of(a.offsets, g, a.T) / R + g; };
         const int g = a.offsets ? last_group(a.S, item, key) : 0;
         const int o0 = bound_of(a.offsets, g, a.T), o1 = bound_of(a.offsets, g + 1, a.T);
@@ -216,72 +230,77 @@ __global__ __launch_bounds__(kBalThreads) void balance_sums(BalanceArgs a, int R
     }
 }
 
-// Sum of the chunk's token counts of group g, by one wave.
-__device__ __forceinline__ int group_tokens(const BalanceWs &w, int i0, int i1) {
-    int n = 0;
-    for (int i = i0 + (int)(threadIdx.x & 63); i < i1; i += 64) n += w.nsum[i];
-    return wave_sum_int(n);
-}
-
-// Block (column tile, group): adds the group's chunks, 64 experts each; the
-// block that finishes last adds the groups' parts of the loss in their order.
+// Block (column tile, group): adds the group's chunks, 64 experts each, a
+// chunk per wave at a time with eight in flight; the block that finishes last
+// has the loss.
 __global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int R, BalanceWs w, BalanceOut o) {
     __shared__ float ps[kBalWaves][64];
     __shared__ int cs[kBalWaves][64];
-    __shared__ int last;
+    __shared__ int ns[kBalWaves];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = a.E;
-    const int g = blockIdx.y, e = blockIdx.x * 64 + lane, ntile = gridDim.x;
+    const int g = blockIdx.y, e = blockIdx.x * 64 + lane;
     const int i0 = bound_of(a.offsets, g, a.T) / R + g, items = a.T / R + a.S;
     const int i1r = g + 1 < a.S ? bound_of(a.offsets, g + 1, a.T) / R + g + 1 : items;
     const int i1 = i1r < items ? i1r : items;
-    const int n = group_tokens(w, i0, i1);
     float p = 0.f;
-    int c = 0;
-    if (e < E) {
-#pragma unroll 8
-        for (int i = i0 + wave; i < i1; i += kBalWaves) {
-            p += w.psum[(size_t)i * E + e];
-            c += w.csum[(size_t)i * E + e];
+    int c = 0, n = 0;
+    for (int i = i0 + tid; i < i1; i += kBalThreads) n += w.nsum[i];
+    const int ec = e < E ? e : E - 1;
+    for (int i = i0 + wave; i < i1; i += 8 * kBalWaves) {
+        float pv[8];
+        int cv[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int at = i + q * kBalWaves < i1 ? i + q * kBalWaves : i;
+            pv[q] = w.psum[(size_t)at * E + ec];
+            cv[q] = w.csum[(size_t)at * E + ec];
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const bool in = i + q * kBalWaves < i1;
+            p += in ? pv[q] : 0.f;
+            c += in ? cv[q] : 0;
         }
     }
+    n = wave_sum_int(n);
     ps[wave][lane] = p;
     cs[wave][lane] = c;
+    if (lane == 0) ns[wave] = n;
     __syncthreads();
-    if (wave == 0) {
-        float v[kBalWaves];
-        c = 0;
+    if (wave != 0) return;
+    float v[kBalWaves];
+    c = 0;
+    n = 0;
 #pragma unroll
-        for (int q = 0; q < kBalWaves; ++q) {
-            v[q] = ps[q][lane];
-            c += cs[q][lane];
-        }
-        p = sum16(v);
-        const float mean = n > 0 ? p / (float)n : 0.0f;
-        if (e < E) {
-            o.counts[(size_t)g * E + e] = c;
-            if (o.prob_mean) o.prob_mean[(size_t)g * E + e] = mean;
-        }
-        const double d = wave_sum_f64(e < E && n > 0 ? (double)c / n * (double)mean : 0.0);
-        if (lane == 0) {
-            w.dot[(size_t)g * ntile + blockIdx.x] = d;
-            if (blockIdx.x == 0) o.n_valid[g] = n;
-            __threadfence();   // the part is visible before the count says so
-            last = atomicAdd(w.done, 1u) == gridDim.x * gridDim.y - 1;
-        }
+    for (int q = 0; q < kBalWaves; ++q) {
+        v[q] = ps[q][lane];
+        c += cs[q][lane];
+        n += ns[q];
     }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    if (wave == 0) {
-        double s = 0.0;
-        int live = 0;
-        for (int q = lane; q < a.S * ntile; q += 64) s += w.dot[q];
-        for (int q = lane; q < a.S; q += 64) live += o.n_valid[q] > 0;
-        s = wave_sum_f64(s);
-        live = wave_sum_int(live);
-        if (lane == 0) {
+    const float mean = n > 0 ? sum16(v) / (float)n : 0.0f;
+    if (e < E) {
+        o.counts[(size_t)g * E + e] = c;
+        if (o.prob_mean) o.prob_mean[(size_t)g * E + e] = mean;
+    }
+    const double d = wave_sum_f64(e < E && n > 0 ? (double)c / n * (double)mean : 0.0);
+    if (lane == 0) {
+        const bool first = blockIdx.x == 0;
+        if (first) o.n_valid[g] = n;
+        // the parts travel in atomics alone; each has happened once its old
+        // value is back, so the block that counts itself last sees them all
+        unsigned long long seen = 0;
+        if (d == d)
+            seen = atomicAdd(w.dot, (unsigned long long)(d * (double)(1ull << kDotBits) + 0.5));
+        else
+            seen = atomicOr(w.nan, 1u);
+        if (first && n > 0) seen += atomicAdd(w.live, 1u);
+        asm volatile("" : "+v"(seen)::"memory");   // waits for the values above
+        if (atomicAdd(w.done, 1u) == gridDim.x * gridDim.y - 1) {
+            const double s = (double)atomicAdd(w.dot, 0ull) / (double)(1ull << kDotBits);
+            const int live = (int)atomicAdd(w.live, 0u);
+            const bool bad = atomicOr(w.nan, 0u) != 0;
             o.n_valid[a.S] = live;
-            *o.loss = live > 0 ? (float)((double)a.alpha * E / a.k * s / live) : 0.0f;
+            *o.loss = bad ? NAN : live > 0 ? (float)((double)a.alpha * E / a.k * s / live) : 0.0f;
         }
     }
 }
