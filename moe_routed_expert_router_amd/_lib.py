@@ -291,36 +291,15 @@ def moe_fingerprint(s: MoeShape, r: MoeResidency, experts, out, stream=None) -> 
 
 
 # ------------------ the norm and the router's training side ------------------
-# Tensors are checked here for type, shape and contiguity (the C entries see
-# addresses only); None stands for NULL.
-def _fit(name: str, t, shape: tuple, dtypes: tuple):
-    if t is None:
-        return None
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
+# The tensors' checks (type, shape, contiguity) and addresses are taken in
+# native code (csrc/bind.cpp, built beside libmoe.so): in Python they cost as
+# much as the launch.  None stands for NULL.
 if torch is not None:
-    _F32, _I32, _B16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
-    _REAL = (torch.bfloat16, torch.float32)
-    _BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
-    _MASK = (torch.uint8, torch.bool)
-    # 8-bit codes and their scales: bytes, or torch's own types of the same bits
-    _CODES, _SCALES = (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
-
-
-def _kind(t) -> int:
-    """moe_out_dtype of a tensor that _fit accepted (None: unused)."""
-    return MOE_OUT_F32 if t is not None and t.dtype is torch.float32 else MOE_OUT_BF16
-
-
-def _ws(ws) -> tuple:
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    from . import _bind
+    _bind.init(_raw_stream, lambda: _stream(None),
+               tuple(ctypes.cast(getattr(lib, n), c_void_p).value for n in (
+                   "moe_rms_norm", "moe_rms_norm_backward", "moe_balance_loss", "moe_balance_loss_backward",
+                   "moe_route_backward")))
 
 
 def moe_train_workspace_bytes(s: MoeShape, n_tokens: int, n_seq: int = 1) -> int:
@@ -330,59 +309,40 @@ def moe_train_workspace_bytes(s: MoeShape, n_tokens: int, n_seq: int = 1) -> int
 def moe_rms_norm(s: MoeShape, x, residual, weight, eps: float, residual_out, y, q_kind: int = MOE_Q_NONE,
                  q_codes=None, q_scales=None, rstd=None, stream=None) -> None:
     """h = x + residual -> residual_out; y = h r weight (bf16); the 8-bit
-    output by q_kind; rstd = r.  x and the residual are float32 or bfloat16."""
-    T, H = x.shape[0], s.hidden
-    p = (_fit("x", x, (T, H), _REAL), _fit("residual", residual, (T, H), _REAL),
-         _fit("weight", weight, (H,), _F32), _fit("residual_out", residual_out, (T, H), _REAL),
-         _fit("y", y, (T, H), _B16), _fit("q_codes", q_codes, (T, H), _CODES),
-         _fit("q_scales", q_scales, (T, H // 32), _SCALES), _fit("rstd", rstd, (T,), _F32))
-    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
-        raise TypeError(f"residual is {residual.dtype} and residual_out {residual_out.dtype}: they must agree")
-    _check(lib.moe_rms_norm(ctypes.byref(s), T, _kind(x), p[0], _kind(residual if residual_out is None else residual_out),
-                            p[1], p[2], eps, p[3], p[4], q_kind, p[5], p[6], p[7], _stream(stream)))
+    output by q_kind; rstd = r.  x and the residual are float32 or bfloat16,
+    codes and scales uint8 or torch's own types of the same bits."""
+    st = _bind.rms_norm(s, x, residual, weight, eps, residual_out, y, q_kind, q_codes, q_scales, rstd,
+                        stream if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def moe_rms_norm_backward(s: MoeShape, dy, dresidual, h, q_codes, q_scales, rstd, weight, token_mask, dx, dweight, ws,
                           stream=None) -> None:
     """dx and dweight from h, or (h None) from the MOE_Q_NORMALIZED checkpoint."""
-    T, H = dy.shape[0], s.hidden
-    p = (_fit("dy", dy, (T, H), _REAL), _fit("dresidual", dresidual, (T, H), _REAL),
-         _fit("h", h, (T, H), _REAL), _fit("q_codes", q_codes, (T, H), _CODES),
-         _fit("q_scales", q_scales, (T, H // 32), _SCALES), _fit("rstd", rstd, (T,), _F32),
-         _fit("weight", weight, (H,), _F32), _fit("token_mask", token_mask, (T,), _MASK),
-         _fit("dx", dx, (T, H), _REAL), _fit("dweight", dweight, (H,), _F32))
-    _check(lib.moe_rms_norm_backward(ctypes.byref(s), T, _kind(dy), p[0], _kind(dresidual), p[1], _kind(h), p[2],
-                                     p[3], p[4], p[5], p[6], p[7], _kind(dx), p[8], p[9], *_ws(ws),
-                                     _stream(stream)))
-
-
-def _n_seq(seq_offsets) -> int:
-    return 1 if seq_offsets is None else seq_offsets.numel() - 1
+    st = _bind.rms_norm_backward(s, dy, dresidual, h, q_codes, q_scales, rstd, weight, token_mask, dx, dweight, ws,
+                                 stream if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def moe_balance_loss(s: MoeShape, logits, topk_ids, token_mask, seq_offsets, alpha: float, loss, counts, n_valid,
                      prob_mean, ws, stream=None) -> None:
     """loss, counts [S][E], n_valid [S+1] and prob_mean [S][E] of S sequences
     (seq_offsets int32 [S+1]; None: one group of all tokens)."""
-    T, E, S = logits.shape[0], s.n_experts, _n_seq(seq_offsets)
-    p = (_fit("logits", logits, (T, E), _F32), _fit("topk_ids", topk_ids, (T, s.top_k), _I32),
-         _fit("token_mask", token_mask, (T,), _MASK),
-         _fit("seq_offsets", seq_offsets, (S + 1,), _I32), _fit("loss", loss, (1,), _F32),
-         _fit("counts", counts, (S, E), _I32), _fit("n_valid", n_valid, (S + 1,), _I32),
-         _fit("prob_mean", prob_mean, (S, E), _F32))
-    _check(lib.moe_balance_loss(ctypes.byref(s), T, p[0], p[1], p[2], p[3], S, alpha, p[4], p[5], p[6], p[7],
-                                *_ws(ws), _stream(stream)))
+    st = _bind.balance_loss(s, logits, topk_ids, token_mask, seq_offsets, alpha, loss, counts, n_valid, prob_mean, ws,
+                            stream if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def moe_balance_loss_backward(s: MoeShape, logits, token_mask, seq_offsets, alpha: float, dloss, counts, n_valid,
                               dlogits, stream=None) -> None:
-    T, E, S = logits.shape[0], s.n_experts, _n_seq(seq_offsets)
-    p = (_fit("logits", logits, (T, E), _F32), _fit("token_mask", token_mask, (T,), _MASK),
-         _fit("seq_offsets", seq_offsets, (S + 1,), _I32), _fit("dloss", dloss, (1,), _F32),
-         _fit("counts", counts, (S, E), _I32), _fit("n_valid", n_valid, (S + 1,), _I32),
-         _fit("dlogits", dlogits, (T, E), _F32))
-    _check(lib.moe_balance_loss_backward(ctypes.byref(s), T, p[0], p[1], p[2], S, alpha, p[3], p[4], p[5], p[6],
-                                         _stream(stream)))
+    """dlogits of moe_balance_loss times dloss (float32 [1]; None: 1)."""
+    st = _bind.balance_loss_backward(s, logits, token_mask, seq_offsets, alpha, dloss, counts, n_valid, dlogits,
+                                     stream if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def moe_route_backward(s: MoeShape, x, q_codes, q_scales, q_weight, w_router, renormalize: bool, logits, topk_ids,
@@ -390,21 +350,11 @@ def moe_route_backward(s: MoeShape, x, q_codes, q_scales, q_weight, w_router, re
     """dx, dw_router and dbias (each None if not wanted) from the gradient of
     the routing weights and / or dlogits_in; the layer's input as x (bfloat16)
     or as a checkpoint of moe_rms_norm."""
-    H, E, k = s.hidden, s.n_experts, s.top_k
-    g = dtopk_w if dtopk_w is not None else dlogits_in
-    if g is None:
-        raise ValueError("dtopk_w or dlogits_in must be given")
-    T = g.shape[0]
-    p = (_fit("x", x, (T, H), _BITS16), _fit("q_codes", q_codes, (T, H), _CODES),
-         _fit("q_scales", q_scales, (T, H // 32), _SCALES), _fit("q_weight", q_weight, (H,), _F32),
-         _fit("w_router", w_router, (E, H), _F32), _fit("logits", logits, (T, E), _F32),
-         _fit("topk_ids", topk_ids, (T, k), _I32), _fit("topk_w", topk_w, (T, k), _F32),
-         _fit("dtopk_w", dtopk_w, (T, k), _F32), _fit("dlogits_in", dlogits_in, (T, E), _F32),
-         _fit("token_mask", token_mask, (T,), _MASK), _fit("dx", dx, (T, H), _REAL),
-         _fit("dw_router", dw_router, (E, H), _F32), _fit("dbias", dbias, (E,), _F32))
-    _check(lib.moe_route_backward(ctypes.byref(s), T, p[0], p[1], p[2], p[3], p[4], int(bool(renormalize)), p[5],
-                                  p[6], p[7], p[8], p[9], p[10], _kind(dx), p[11], p[12], p[13], *_ws(ws),
-                                  _stream(stream)))
+    st = _bind.route_backward(s, x, q_codes, q_scales, q_weight, w_router, bool(renormalize), logits, topk_ids, topk_w,
+                              dtopk_w, dlogits_in, token_mask, dx, dw_router, dbias, ws,
+                              stream if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def moe_profile_enable(on: bool) -> None:

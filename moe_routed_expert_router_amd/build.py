@@ -6,14 +6,17 @@
 
 Every .hip source under csrc/ is compiled with hipcc for gfx950 only and
 linked into moe_routed_expert_router_amd/libmoe.so.  Packed fp32 vector ops
-are disabled for all device code.
+are disabled for all device code.  csrc/bind.cpp (host code, the Python
+marshalling of some entries) becomes _bind.so beside it where torch is there.
 """
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -44,11 +47,31 @@ def _compile(src):
     return obj, err
 
 
+def build_bind():
+    """_bind.so against the installed torch's headers; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch_dir = os.path.dirname(spec.origin)
+    out = os.path.join(HERE, "_bind.so")
+    tmp = out + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-isystem", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "bind.cpp"), "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", f"-Wl,-rpath,{os.path.join(torch_dir, 'lib')}", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(jobs=None, verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4, 16)
     with cf.ThreadPoolExecutor(jobs) as ex:
+        bind = ex.submit(build_bind)
         results = list(ex.map(_compile, srcs))
     for obj, err in results:
         if err and verbose:
@@ -59,6 +82,7 @@ def build(jobs=None, verbose=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    bind.result()
     return LIB
 
 

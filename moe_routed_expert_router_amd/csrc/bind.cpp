@@ -1,0 +1,386 @@
+// Python marshalling of the norm and of the router's training side: checks the
+// tensors' types, shapes and contiguity, takes their addresses and calls the
+// C entry.  The same work in Python costs about 3 us a call, as much as the
+// launch it stands before; here it is about 0.5.  _lib.py hands in the entries'
+// addresses (init) and turns a status into MoeError.
+//
+// Every function takes its arguments by position as _lib.py passes them and
+// returns the entry's status; a tensor that does not fit is a TypeError or a
+// ValueError.  None stands for NULL.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <initializer_list>
+
+#include "../../include/moe.h"
+
+namespace {
+
+using at::ScalarType;
+
+enum : unsigned {
+    kF32 = 1, kB16 = 2, kI32 = 4, kU8 = 8, kBool = 16, kI16 = 32, kU16 = 64, kE4M3 = 128, kE8M0 = 256,
+    kReal = kF32 | kB16, kMask = kU8 | kBool, kCodes = kU8 | kE4M3, kScales = kU8 | kE8M0,
+    kBits16 = kB16 | kI16 | kU16
+};
+
+struct Type {
+    unsigned bit;
+    ScalarType type;
+    const char *name;
+};
+const Type kTypes[] = {
+    {kF32, ScalarType::Float, "torch.float32"},         {kB16, ScalarType::BFloat16, "torch.bfloat16"},
+    {kI32, ScalarType::Int, "torch.int32"},             {kU8, ScalarType::Byte, "torch.uint8"},
+    {kBool, ScalarType::Bool, "torch.bool"},            {kI16, ScalarType::Short, "torch.int16"},
+    {kU16, ScalarType::UInt16, "torch.uint16"},         {kE4M3, ScalarType::Float8_e4m3fn, "torch.float8_e4m3fn"},
+    {kE8M0, ScalarType::Float8_e8m0fnu, "torch.float8_e8m0fnu"},
+};
+
+decltype(&moe_rms_norm) g_rms_norm;
+decltype(&moe_rms_norm_backward) g_rms_norm_backward;
+decltype(&moe_balance_loss) g_balance_loss;
+decltype(&moe_balance_loss_backward) g_balance_loss_backward;
+decltype(&moe_route_backward) g_route_backward;
+PyObject *g_raw_stream;   // device index -> raw handle of its current stream, or None
+PyObject *g_stream;       // () -> raw handle, when there is no other way
+
+// One call's arguments.  After the first misfit `ok` is false and a Python
+// error is set.
+struct Call {
+    PyObject *const *args;
+    Py_ssize_t n;
+    bool ok = true;
+    int device = -1;
+    moe_shape shape{};
+
+    Call(PyObject *const *a, Py_ssize_t got, Py_ssize_t want) : args(a), n(got) {
+        if (got != want) {
+            PyErr_Format(PyExc_TypeError, "%zd arguments, expected %zd", got, want);
+            ok = false;
+            return;
+        }
+        Py_buffer b;
+        if (PyObject_GetBuffer(a[0], &b, PyBUF_SIMPLE) != 0) {
+            ok = false;
+            return;
+        }
+        if (b.len == (Py_ssize_t)sizeof(moe_shape)) {
+            memcpy(&shape, b.buf, sizeof(moe_shape));
+        } else {
+            PyErr_SetString(PyExc_TypeError, "the first argument must be a MoeShape");
+            ok = false;
+        }
+        PyBuffer_Release(&b);
+    }
+
+    const at::Tensor *tensor(int i, const char *name) {
+        if (!ok || args[i] == Py_None) return nullptr;
+        if (!THPVariable_Check(args[i])) {
+            PyErr_Format(PyExc_TypeError, "%s must be a tensor or None, got %s", name, Py_TYPE(args[i])->tp_name);
+            ok = false;
+            return nullptr;
+        }
+        return &THPVariable_Unpack(args[i]);
+    }
+
+    // Rows of argument i (-1: not there).
+    int64_t rows(int i, const char *name) {
+        const at::Tensor *t = tensor(i, name);
+        if (!ok || !t) return -1;
+        if (t->dim() < 1) {
+            PyErr_Format(PyExc_ValueError, "%s has no dimension", name);
+            ok = false;
+            return -1;
+        }
+        return t->size(0);
+    }
+
+    // Address of argument i, a contiguous tensor [d0] (d1 < 0) or [d0][d1] of
+    // one of the types; *type gets its type's bit.
+    void *fit(int i, const char *name, unsigned types, int64_t d0, int64_t d1, unsigned *type = nullptr) {
+        if (type) *type = 0;
+        const at::Tensor *t = tensor(i, name);
+        if (!ok || !t) return nullptr;
+        const ScalarType st = t->scalar_type();
+        unsigned bit = 0;
+        for (const Type &k : kTypes)
+            if (k.type == st) bit = k.bit & types;
+        if (!bit) {
+            char want[160] = "";
+            for (const Type &k : kTypes)
+                if (k.bit & types) {
+                    if (want[0]) strncat(want, " or ", sizeof(want) - strlen(want) - 1);
+                    strncat(want, k.name, sizeof(want) - strlen(want) - 1);
+                }
+            PyErr_Format(PyExc_TypeError, "%s must be %s, got %s", name, want, c10::toString(st));
+            ok = false;
+            return nullptr;
+        }
+        const bool one = d1 < 0;
+        if (t->dim() != (one ? 1 : 2) || t->size(0) != d0 || (!one && t->size(1) != d1)) {
+            if (one)
+                PyErr_Format(PyExc_ValueError, "%s must have shape (%lld,)", name, (long long)d0);
+            else
+                PyErr_Format(PyExc_ValueError, "%s must have shape (%lld, %lld)", name, (long long)d0, (long long)d1);
+            ok = false;
+            return nullptr;
+        }
+        if (!t->is_contiguous()) {
+            PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
+            ok = false;
+            return nullptr;
+        }
+        if (device < 0 && t->is_cuda()) device = t->get_device();
+        if (type) *type = bit;
+        return t->data_ptr();
+    }
+
+    // Address and bytes of a workspace tensor of any type.
+    void *workspace(int i, size_t *bytes) {
+        *bytes = 0;
+        const at::Tensor *t = tensor(i, "ws");
+        if (!ok || !t) return nullptr;
+        *bytes = t->nbytes();
+        return t->data_ptr();
+    }
+
+    double number(int i) {
+        if (!ok) return 0.0;
+        const double v = PyFloat_AsDouble(args[i]);
+        if (v == -1.0 && PyErr_Occurred()) ok = false;
+        return v;
+    }
+    int integer(int i) {
+        if (!ok) return 0;
+        const long v = PyLong_AsLong(args[i]);
+        if (v == -1 && PyErr_Occurred()) ok = false;
+        if (ok && (v < INT32_MIN || v > INT32_MAX)) {
+            PyErr_SetString(PyExc_OverflowError, "argument outside int32");
+            ok = false;
+        }
+        return (int)v;
+    }
+
+    // Raw stream of argument i: an int, or None for the current stream.
+    void *stream(int i) {
+        if (!ok) return nullptr;
+        PyObject *r;
+        if (args[i] != Py_None) {
+            r = args[i];
+            Py_INCREF(r);
+        } else if (device >= 0 && g_raw_stream != Py_None) {
+            PyObject *d = PyLong_FromLong(device);
+            r = d ? PyObject_CallOneArg(g_raw_stream, d) : nullptr;
+            Py_XDECREF(d);
+        } else {
+            r = PyObject_CallNoArgs(g_stream);
+        }
+        void *p = nullptr;
+        if (r && r != Py_None) p = PyLong_AsVoidPtr(r);
+        if (!r || (p == nullptr && PyErr_Occurred())) ok = false;
+        Py_XDECREF(r);
+        return p;
+    }
+};
+
+int32_t dtype(unsigned bit) { return bit == kF32 ? MOE_OUT_F32 : MOE_OUT_BF16; }
+
+template <typename F>
+PyObject *guarded(F &&f) {
+    try {
+        return f();
+    } catch (const std::exception &e) {   // a tensor without storage or of another layout
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, e.what());
+    } catch (...) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "unusable argument");
+    }
+    return nullptr;
+}
+
+#define CALL_ENTRY(status, expr)  \
+    moe_status status;            \
+    Py_BEGIN_ALLOW_THREADS        \
+    status = (expr);              \
+    Py_END_ALLOW_THREADS
+
+bool check_rows(Call &c, int64_t t, const char *name) {
+    if (!c.ok) return false;
+    if (t < 0) {
+        PyErr_Format(PyExc_TypeError, "%s must be given", name);
+        return false;
+    }
+    if (t > INT32_MAX) {
+        PyErr_Format(PyExc_ValueError, "%s has %lld rows", name, (long long)t);
+        return false;
+    }
+    return true;
+}
+
+// s, x, residual, weight, eps, residual_out, y, q_kind, q_codes, q_scales, rstd, stream
+PyObject *rms_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Call c(args, n, 12);
+        const int64_t T = c.ok ? c.rows(1, "x") : -1, H = c.shape.hidden;
+        if (!check_rows(c, T, "x")) return nullptr;
+        unsigned xt, rt, ot;
+        void *x = c.fit(1, "x", kReal, T, H, &xt), *res = c.fit(2, "residual", kReal, T, H, &rt);
+        void *w = c.fit(3, "weight", kF32, H, -1);
+        const float eps = (float)c.number(4);
+        void *ro = c.fit(5, "residual_out", kReal, T, H, &ot), *y = c.fit(6, "y", kB16, T, H);
+        const int kind = c.integer(7);
+        void *qc = c.fit(8, "q_codes", kCodes, T, H), *qs = c.fit(9, "q_scales", kScales, T, H / 32);
+        void *r = c.fit(10, "rstd", kF32, T, -1);
+        if (c.ok && rt && ot && rt != ot) {
+            PyErr_SetString(PyExc_TypeError, "residual and residual_out must be of one type");
+            return nullptr;
+        }
+        void *st = c.stream(11);
+        if (!c.ok) return nullptr;
+        CALL_ENTRY(s, g_rms_norm(&c.shape, (int32_t)T, dtype(xt), x, dtype(ot ? ot : rt), res, (const float *)w, eps, ro,
+                                 (uint16_t *)y, kind, (uint8_t *)qc, (uint8_t *)qs, (float *)r, st));
+        return PyLong_FromLong(s);
+    });
+}
+
+// s, dy, dresidual, h, q_codes, q_scales, rstd, weight, token_mask, dx, dweight, ws, stream
+PyObject *rms_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Call c(args, n, 13);
+        const int64_t T = c.ok ? c.rows(1, "dy") : -1, H = c.shape.hidden;
+        if (!check_rows(c, T, "dy")) return nullptr;
+        unsigned yt, rt, ht, xt;
+        void *dy = c.fit(1, "dy", kReal, T, H, &yt), *dr = c.fit(2, "dresidual", kReal, T, H, &rt);
+        void *h = c.fit(3, "h", kReal, T, H, &ht);
+        void *qc = c.fit(4, "q_codes", kCodes, T, H), *qs = c.fit(5, "q_scales", kScales, T, H / 32);
+        void *r = c.fit(6, "rstd", kF32, T, -1), *w = c.fit(7, "weight", kF32, H, -1);
+        void *m = c.fit(8, "token_mask", kMask, T, -1);
+        void *dx = c.fit(9, "dx", kReal, T, H, &xt), *dw = c.fit(10, "dweight", kF32, H, -1);
+        size_t bytes;
+        void *ws = c.workspace(11, &bytes), *st = c.stream(12);
+        if (!c.ok) return nullptr;
+        CALL_ENTRY(s, g_rms_norm_backward(&c.shape, (int32_t)T, dtype(yt), dy, dtype(rt), dr, dtype(ht), h,
+                                          (const uint8_t *)qc, (const uint8_t *)qs, (const float *)r, (const float *)w,
+                                          (const uint8_t *)m, dtype(xt), dx, (float *)dw, ws, bytes, st));
+        return PyLong_FromLong(s);
+    });
+}
+
+// Sequences of an offsets argument: 1 for None.
+int64_t sequences(Call &c, int i) {
+    const int64_t r = c.rows(i, "seq_offsets");
+    return r < 0 ? 1 : r - 1;
+}
+
+// s, logits, topk_ids, token_mask, seq_offsets, alpha, loss, counts, n_valid, prob_mean, ws, stream
+PyObject *balance_loss(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Call c(args, n, 12);
+        const int64_t T = c.ok ? c.rows(1, "logits") : -1, E = c.shape.n_experts;
+        if (!check_rows(c, T, "logits")) return nullptr;
+        const int64_t S = sequences(c, 4);
+        if (!c.ok) return nullptr;
+        void *z = c.fit(1, "logits", kF32, T, E), *ids = c.fit(2, "topk_ids", kI32, T, c.shape.top_k);
+        void *m = c.fit(3, "token_mask", kMask, T, -1), *off = c.fit(4, "seq_offsets", kI32, S + 1, -1);
+        const float alpha = (float)c.number(5);
+        void *loss = c.fit(6, "loss", kF32, 1, -1), *cnt = c.fit(7, "counts", kI32, S, E);
+        void *nv = c.fit(8, "n_valid", kI32, S + 1, -1), *pm = c.fit(9, "prob_mean", kF32, S, E);
+        size_t bytes;
+        void *ws = c.workspace(10, &bytes), *st = c.stream(11);
+        if (!c.ok) return nullptr;
+        CALL_ENTRY(s, g_balance_loss(&c.shape, (int32_t)T, (const float *)z, (const int32_t *)ids, (const uint8_t *)m,
+                                     (const int32_t *)off, (int32_t)S, alpha, (float *)loss, (int32_t *)cnt,
+                                     (int32_t *)nv, (float *)pm, ws, bytes, st));
+        return PyLong_FromLong(s);
+    });
+}
+
+// s, logits, token_mask, seq_offsets, alpha, dloss, counts, n_valid, dlogits, stream
+PyObject *balance_loss_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Call c(args, n, 10);
+        const int64_t T = c.ok ? c.rows(1, "logits") : -1, E = c.shape.n_experts;
+        if (!check_rows(c, T, "logits")) return nullptr;
+        const int64_t S = sequences(c, 3);
+        if (!c.ok) return nullptr;
+        void *z = c.fit(1, "logits", kF32, T, E), *m = c.fit(2, "token_mask", kMask, T, -1);
+        void *off = c.fit(3, "seq_offsets", kI32, S + 1, -1);
+        const float alpha = (float)c.number(4);
+        void *dl = c.fit(5, "dloss", kF32, 1, -1), *cnt = c.fit(6, "counts", kI32, S, E);
+        void *nv = c.fit(7, "n_valid", kI32, S + 1, -1), *dz = c.fit(8, "dlogits", kF32, T, E);
+        void *st = c.stream(9);
+        if (!c.ok) return nullptr;
+        CALL_ENTRY(s, g_balance_loss_backward(&c.shape, (int32_t)T, (const float *)z, (const uint8_t *)m,
+                                              (const int32_t *)off, (int32_t)S, alpha, (const float *)dl,
+                                              (const int32_t *)cnt, (const int32_t *)nv, (float *)dz, st));
+        return PyLong_FromLong(s);
+    });
+}
+
+// s, x, q_codes, q_scales, q_weight, w_router, renormalize, logits, topk_ids, topk_w, dtopk_w, dlogits_in, token_mask,
+// dx, dw_router, dbias, ws, stream
+PyObject *route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Call c(args, n, 18);
+        if (!c.ok) return nullptr;
+        int64_t T = c.rows(10, "dtopk_w");
+        if (c.ok && T < 0) T = c.rows(11, "dlogits_in");
+        if (!c.ok) return nullptr;
+        if (T < 0) {
+            PyErr_SetString(PyExc_ValueError, "dtopk_w or dlogits_in must be given");
+            return nullptr;
+        }
+        if (!check_rows(c, T, "the gradient")) return nullptr;
+        const int64_t H = c.shape.hidden, E = c.shape.n_experts, k = c.shape.top_k;
+        unsigned xt;
+        void *x = c.fit(1, "x", kBits16, T, H), *qc = c.fit(2, "q_codes", kCodes, T, H);
+        void *qs = c.fit(3, "q_scales", kScales, T, H / 32), *qw = c.fit(4, "q_weight", kF32, H, -1);
+        void *wr = c.fit(5, "w_router", kF32, E, H);
+        const int renorm = c.integer(6);
+        void *z = c.fit(7, "logits", kF32, T, E), *ids = c.fit(8, "topk_ids", kI32, T, k);
+        void *w = c.fit(9, "topk_w", kF32, T, k), *dw = c.fit(10, "dtopk_w", kF32, T, k);
+        void *dz = c.fit(11, "dlogits_in", kF32, T, E), *m = c.fit(12, "token_mask", kMask, T, -1);
+        void *dx = c.fit(13, "dx", kReal, T, H, &xt), *dwr = c.fit(14, "dw_router", kF32, E, H);
+        void *db = c.fit(15, "dbias", kF32, E, -1);
+        size_t bytes;
+        void *ws = c.workspace(16, &bytes), *st = c.stream(17);
+        if (!c.ok) return nullptr;
+        CALL_ENTRY(s, g_route_backward(&c.shape, (int32_t)T, (const uint16_t *)x, (const uint8_t *)qc,
+                                       (const uint8_t *)qs, (const float *)qw, (const float *)wr, renorm,
+                                       (const float *)z, (const int32_t *)ids, (const float *)w, (const float *)dw,
+                                       (const float *)dz, (const uint8_t *)m, dtype(xt), dx, (float *)dwr, (float *)db,
+                                       ws, bytes, st));
+        return PyLong_FromLong(s);
+    });
+}
+
+// init(raw_stream, stream, addresses): addresses of the entries in the order below
+PyObject *init(PyObject *, PyObject *args) {
+    PyObject *raw, *stream;
+    unsigned long long a[5];
+    if (!PyArg_ParseTuple(args, "OO(KKKKK)", &raw, &stream, &a[0], &a[1], &a[2], &a[3], &a[4])) return nullptr;
+    Py_INCREF(raw);
+    Py_INCREF(stream);
+    g_raw_stream = raw;
+    g_stream = stream;
+    g_rms_norm = (decltype(g_rms_norm))(uintptr_t)a[0];
+    g_rms_norm_backward = (decltype(g_rms_norm_backward))(uintptr_t)a[1];
+    g_balance_loss = (decltype(g_balance_loss))(uintptr_t)a[2];
+    g_balance_loss_backward = (decltype(g_balance_loss_backward))(uintptr_t)a[3];
+    g_route_backward = (decltype(g_route_backward))(uintptr_t)a[4];
+    Py_RETURN_NONE;
+}
+
+PyMethodDef kMethods[] = {
+    {"init", init, METH_VARARGS, nullptr},
+    {"rms_norm", (PyCFunction)(void *)rms_norm, METH_FASTCALL, nullptr},
+    {"rms_norm_backward", (PyCFunction)(void *)rms_norm_backward, METH_FASTCALL, nullptr},
+    {"balance_loss", (PyCFunction)(void *)balance_loss, METH_FASTCALL, nullptr},
+    {"balance_loss_backward", (PyCFunction)(void *)balance_loss_backward, METH_FASTCALL, nullptr},
+    {"route_backward", (PyCFunction)(void *)route_backward, METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__bind(void) { return PyModule_Create(&kModule); }
