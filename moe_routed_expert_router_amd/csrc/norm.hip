@@ -309,24 +309,29 @@ __global__ __launch_bounds__(1024) void rms_norm_backward(NormBwdArgs a, float *
     }
 }
 
-// Column sums: block = 64 columns, eight waves take the rows w, w + 8, ...
-__global__ __launch_bounds__(512) void column_sum(const float *__restrict__ part, int R, int C,
-                                                  float *__restrict__ out) {
-    __shared__ float lds[8][64];
+// Column sums: block = 64 columns, sixteen waves take the rows w, w + 16, ...,
+// eight in flight each.
+__global__ __launch_bounds__(1024) void column_sum(const float *__restrict__ part, int R, int C,
+                                                   float *__restrict__ out) {
+    __shared__ float lds[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    const int c = blockIdx.x * 64 + lane, cc = c < C ? c : C - 1;
     float s = 0.f;
-    if (c < C) {
-#pragma unroll 8
-        for (int r = wave; r < R; r += 8) s += part[(size_t)r * C + c];
+    for (int r = wave; r < R; r += 128) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = part[(size_t)(r + 16 * i < R ? r + 16 * i : r) * C + cc];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += r + 16 * i < R ? v[i] : 0.f;
     }
     lds[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && c < C) {
-        float v[8];
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = lds[i][lane];
-        out[c] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        for (int i = 0; i < 4; ++i)
+            v[i] = (lds[4 * i][lane] + lds[4 * i + 1][lane]) + (lds[4 * i + 2][lane] + lds[4 * i + 3][lane]);
+        out[c] = (v[0] + v[1]) + (v[2] + v[3]);
     }
 }
 
@@ -365,7 +370,7 @@ void bwd_dy(const NormBwdArgs &a, int waves, float *part, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_column_sum(const char *name, const float *part, int R, int C, float *out, hipStream_t st) {
-    MOE_LAUNCH(name, column_sum, dim3((C + 63) / 64), dim3(512), 0, st, part, R, C, out);
+    MOE_LAUNCH(name, column_sum, dim3((C + 63) / 64), dim3(1024), 0, st, part, R, C, out);
     return hipGetLastError();
 }
 

@@ -213,23 +213,31 @@ __device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[
     }
 }
 
-// 32 columns of Wr [E][H] as scaled units (32 hidden columns, 16 experts):
-// first the columns' maxima, then, from the cache, the values.  Group 2 b + o
-// holds the columns 64 b + o, 64 b + o + 2, ...: a lane of the product then has
-// two neighbouring columns, which it stores as one.
+// 32 columns of Wr [E][H] as scaled units (32 hidden columns, 16 experts), the
+// values in registers between the columns' maxima and the conversion.  Group
+// 2 b + o holds the columns 64 b + o, 64 b + o + 2, ...: a lane of the product
+// then has two neighbouring columns, which it stores as one.
 template <int NP>
 __device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int32_t *__restrict__ hscale, int EC, int hg,
                          float *lds) {
+    constexpr int kMost = kMaxExperts / 16 / 16;   // units per wave
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int h = 64 * (hg >> 1) + (hg & 1) + 2 * (lane & 31);
     const float *col = a.wr + h;
-    float m = 0.f;
-#pragma unroll 4
-    for (int e = tid >> 5; e < a.E; e += 32) {
-        // NaN and infinities count as infinite: the column is not scaled
-        const float v = fabsf(col[(size_t)e * a.H]);
-        m = v < INFINITY ? fmaxf(m, v) : INFINITY;
+    float v[kMost][8], m = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        const int e0 = 16 * (wave + 16 * j) + 8 * (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = e0 + i < a.E ? col[(size_t)(e0 + i) * a.H] : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = fabsf(v[j][i]);   // a NaN or an infinity: the column is not scaled
+            m = u < INFINITY ? fmaxf(m, u) : INFINITY;
+        }
     lds[tid] = m;
     __syncthreads();
     m = 0.f;
@@ -237,15 +245,14 @@ __device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int32
     for (int r = 0; r < 32; ++r) m = fmaxf(m, lds[32 * r + (lane & 31)]);
     const int sc = scale_exponent(m);
     if (tid < 32) hscale[h] = sc;
-    for (int ec = wave; ec < EC; ec += 16) {
-        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = 16 * ec + 8 * (lane >> 5) + i;
-            v[i] = e < a.E ? ldexpf(col[(size_t)e * a.H], sc) : 0.f;
-        }
+    for (int j = 0; j < kMost; ++j) {
+        const int ec = wave + 16 * j;
+        if (ec >= EC) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = ldexpf(v[j][i], sc);
         uint4 o[NP];
-        split8_f16<NP>(v, o);
+        split8_f16<NP>(v[j], o);
 #pragma unroll
         for (int q = 0; q < NP; ++q)
             *reinterpret_cast<uint4 *>(out + (((size_t)hg * EC + ec) * NP + q) * kUnit + 16 * lane) = o[q];
@@ -863,7 +870,10 @@ __global__ __launch_bounds__(256) void route_zero(float *p, size_t n) {
 // products: dz as fp32 rows [T][E8] (E rounded up to 8, zeros past E), and
 // both products straight from the fp32 operands on the 32x32x2 fp32 MFMA, in
 // one launch whose blocks have one of three roles (dx, dWr, db).
-constexpr int kFewTokens = 32;
+// H 4096, E 384: 12 against 31 us at 32 and 48 tokens, 31 against 35 at 128
+// (fp32 dx: 31 against 44), 44 against 38 at 192; H 1024, E 64: 24 against 26
+// us at 128.
+constexpr int kFewTokens = 128;
 
 template <int NPL>
 __global__ __launch_bounds__(256) void route_dz_rows(RouteBwdArgs a, float *__restrict__ dz, int E8) {

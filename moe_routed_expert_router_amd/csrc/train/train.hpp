@@ -71,8 +71,8 @@ struct RouteBwdArgs {
 size_t route_bwd_ws_bytes(int T, int H, int E);
 hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st);
 
-// out[c] = sum over r of part[r][c] in row order of four interleaved chains
-// (fixed for a given R); part [R][C].  R = 0 writes zeros.
+// out[c] = sum over r of part[r][c] in sixteen interleaved chains of rows
+// (a fixed order for a given R); part [R][C].  R = 0 writes zeros.
 hipError_t launch_column_sum(const char *name, const float *part, int R, int C, float *out, hipStream_t st);
 
 // CALL(N) with N >= ceil(E / 64) logits per lane of a wave.

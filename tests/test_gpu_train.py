@@ -392,21 +392,22 @@ class Route:
         wx, ww, wb = ot.route_backward(dz, np.where(keep[:, None], self.xv, 0), f64(self.wr), m)
         W, X, Z = np.abs(f64(self.wr)), np.abs(np.where(keep[:, None], self.xv, 0)), np.abs(dz)
         Ep = -(-E // 32) * 32
-        # dx above 32 tokens: fp16 terms of factors scaled per row (dz) and
+        # dx above 128 tokens: fp16 terms of factors scaled per row (dz) and
         # column (Wr) to a largest magnitude of 2^14 or more.  A term leaves
         # 2^-11 of the value, two leave 2^-22, and what is under half of fp16's
         # least step, 2^-25, i.e. 2^-39 of the largest.  bf16 out: one term,
         # |zw - z1 w1| <= (2 2^-11 + 2^-22) |z||w|.  fp32 out: hi hi + hi lo +
-        # lo hi: 2 2^-22 left of the factors and lo lo <= 2^-22.  Up to 32 tokens
+        # lo hi: 2 2^-22 left of the factors and lo lo <= 2^-22.  Up to 128 tokens
         # the products are fp32's.  The accumulation rounds once for each of
         # nprod Ep additions (2 U: a matrix core may truncate).
         one = self.dx.dtype == B16
         split, nprod = (2.001 * 2.0 ** -11, 1) if one else (3 * 2.0 ** -22, 3)
         floor = 2.0 ** -38 * (Z.max(1, keepdims=True) * W.sum(0) + Z.sum(1, keepdims=True) * W.max(0))
-        if T <= 32:
-            split, nprod, floor = U, 1, 0
+        if T <= 128:
+            split, nprod, floor = U, 1, (Ep + 32) * 2.0 ** -150
         b = err @ W + (split + 2 * U * nprod * (Ep + 32)) * (Z @ W) + floor
-        # and half the least step that the stored type has: 2^-133 (bf16), 2^-149 (fp32)
+        # and half the least step that the stored type has: 2^-133 (bf16),
+        # 2^-149 (fp32); in the unscaled fp32 sums every addition may lose that
         close(self.dx, wx, b + (UB if one else U) * (np.abs(wx) + b) + (2.0 ** -134 if one else 2.0 ** -150))
         n = 3 * (-(-T // 32) * 32) + 16
         close(self.dwr, ww, err.T @ X + (2.0 ** -24 + 2 * U * n + 2 * U) * (Z.T @ X))
@@ -415,7 +416,8 @@ class Route:
 
 @pytest.mark.parametrize("src,renorm,dxt", [("x", True, B16), ("x", False, F32), ("q_norm", True, F32), ("q_out", False, B16)])
 @pytest.mark.parametrize("T,H,E,k", [(1, 128, 8, 2), (4, 256, 8, 2), (33, 384, 40, 3), (130, 128, 257, 8), (64, 640, 1, 1),
-                                     (300, 1024, 130, 4), (40, 256, 1024, 32)])
+                                     (300, 1024, 130, 4), (40, 256, 1024, 32), (128, 256, 33, 2), (129, 384, 40, 3),
+                                     (140, 256, 1024, 32), (161, 896, 385, 6), (256, 128, 8, 2)])
 def test_route_backward(T, H, E, k, src, renorm, dxt):
     c = Route(T, H, E, k, src, renorm, mask=T > 4, dxt=dxt, seed=T)
     c.run()
@@ -454,13 +456,14 @@ def test_route_backward_dropped_and_repeated_ids(renorm):
     c.check()
 
 
+@pytest.mark.parametrize("T", [90, 150])
 @pytest.mark.parametrize("dxt", [B16, F32])
-def test_route_backward_magnitudes(dxt):
+def test_route_backward_magnitudes(dxt, T):
     """Rows of dz and columns of Wr over many decades, within and between rows:
     the scaling keeps every row's own precision."""
-    c = Route(90, 256, 72, 3, "x", True, dw=False, dxt=dxt)
+    c = Route(T, 256, 72, 3, "x", True, dw=False, dxt=dxt)
     g = torch.Generator().manual_seed(3)
-    c.dz *= 10.0 ** (torch.rand((90, 1), generator=g) * 40 - 30).cuda()
+    c.dz *= 10.0 ** (torch.rand((T, 1), generator=g) * 40 - 30).cuda()
     c.dz[:45] *= 10.0 ** -(torch.rand((45, 72), generator=g) * 9).cuda()
     c.dz[3] = 0
     c.wr *= 10.0 ** (torch.rand((1, 256), generator=g) * 20 - 15).cuda()
@@ -470,10 +473,11 @@ def test_route_backward_magnitudes(dxt):
     c.check()
 
 
-def test_route_backward_nonfinite_rows():
+@pytest.mark.parametrize("T", [70, 140])
+def test_route_backward_nonfinite_rows(T):
     """A non-finite entry makes its own row (or column) non-finite and no other."""
     for dxt in (B16, F32):
-        c = Route(70, 256, 40, 3, "x", True, dw=False, dxt=dxt)
+        c = Route(T, 256, 40, 3, "x", True, dw=False, dxt=dxt)
         c.dz[4, 7] = float("inf")
         c.dz[40, 0] = float("nan")
         c.wr[9, 200] = float("-inf")
