@@ -18,15 +18,16 @@ namespace {
 
 constexpr int kNormMaxWaves = 16;
 
-// Waves per row and chunks of 8 elements per lane for a row of H elements:
-// two chunks (32 bytes of bf16, two loads in flight per stream) up to 16 waves
-// of them, then eight.
-struct RowShape {
-    int v, waves;
-};
-RowShape row_shape(int H) {
-    if (H <= 2 * 8 * kWave * kNormMaxWaves) return {2, (H + 2 * 8 * kWave - 1) / (2 * 8 * kWave)};
-    return {8, (H + 8 * 8 * kWave - 1) / (8 * 8 * kWave)};
+// Chunks of 8 elements that a lane keeps in registers (32 bytes of bf16: two
+// loads in flight per stream), and waves per row: up to 16384 elements a row
+// stays in registers between its reads and its writes; longer rows are read
+// twice (the *_wide kernels).
+constexpr int kV = 2;
+constexpr int kNormRow = kV * 8 * kWave * kNormMaxWaves;
+
+int row_waves(int H) {
+    const int n = (H + kV * 8 * kWave - 1) / (kV * 8 * kWave);
+    return n < kNormMaxWaves ? n : kNormMaxWaves;
 }
 
 // A double as the float with the same leading 21 significant bits, the last
@@ -85,108 +86,177 @@ __device__ __forceinline__ uint2 mx_encode(const float *f, uint32_t *scale) {
 __device__ __forceinline__ float as_stored(float, float v) { return v; }
 __device__ __forceinline__ float as_stored(Bf16, float v) { return (float)(__bf16)v; }
 
+// Sum of a double over the block; every thread gets it.
+__device__ __forceinline__ double block_sum_f64(double s, double *part) {
+    s = wave_sum_f64(s);
+    if (blockDim.x > kWave) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+        __syncthreads();
+        s = 0.0;
+        for (int w = 0; w < (int)blockDim.x / kWave; ++w) s += part[w];
+    }
+    return s;
+}
+
+// h of eight elements, and their squares into s.
+template <typename X, typename R>
+__device__ __forceinline__ void norm_sum(const Raw8<X> &rx, const Raw8<R> &rr, bool res, float *h, double &s) {
+    rx.get(h);
+    if (res) {
+        float r[8];
+        rr.get(r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = as_stored(R{}, h[i] + r[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = as_stored(R{}, h[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double d = (double)h[i];
+        s = fma(d, d, s);
+    }
+}
+
+// Outputs of chunk c of the row that starts at `base` (in: the chunk is in the
+// row; every lane calls it, as four lanes share a block of 32).
+__device__ __forceinline__ void norm_out(const NormArgs &a, size_t base, int c, bool in, const float *h, const float *w,
+                                         double r) {
+    float y[8];
+    if (a.q_kind == MOE_Q_NONE) {
+        const float rf = (float)r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = h[i] * rf * w[i];
+    } else {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double n = (double)h[i] * r;
+            const float v = sticky_f32(n * (double)w[i]);
+            q[i] = a.q_kind == MOE_Q_OUTPUT ? v : sticky_f32(n);
+            y[i] = v;
+        }
+        uint32_t sc;
+        const uint2 codes = mx_encode(q, &sc);   // H % 32 == 0: the four lanes of a block are in or out together
+        if (in) {
+            *reinterpret_cast<uint2 *>(a.codes + base + 8 * c) = codes;
+            if ((c & 3) == 0) a.scales[(base >> 5) + (c >> 2)] = (uint8_t)sc;
+        }
+    }
+    if (a.y && in) store8(Bf16{}, a.y, base + 8 * c, y);
+}
+
 // One block per token, the row in registers.  The square sum and the 8-bit
 // output's values are in 64 bits: the sum cannot overflow whatever the type
 // holds, and a code is the one the exact value rounds to.
-template <int V, typename X, typename R>
-__global__ __launch_bounds__(1024) void rms_norm(NormArgs a) {
+template <typename X, typename R>
+__global__ __launch_bounds__(kWave *kNormMaxWaves) void rms_norm(NormArgs a) {
     __shared__ double part[kNormMaxWaves];
     const size_t row = blockIdx.x;
     const int tid = threadIdx.x, nthr = blockDim.x, nch = a.H / 8;
     const size_t base = row * (size_t)a.H;
-    Raw8<X> rx[V];
-    Raw8<R> rr[V];
-    Raw8<float> rw[V];
+    Raw8<X> rx[kV];
+    Raw8<R> rr[kV];
+    Raw8<float> rw[kV];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < kV; ++j) {
         const int c = tid + j * nthr;
+        rr[j].zero();
         if (c < nch) {
             rx[j].load(a.x, base + 8 * c);
             if (a.res) rr[j].load(a.res, base + 8 * c);
             rw[j].load(a.weight, 8 * c);
         } else {
             rx[j].zero();
-            rr[j].zero();
             rw[j].zero();
         }
     }
-    float h[V][8];
+    float h[kV][8];
     double s = 0.0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        rx[j].get(h[j]);
-        if (a.res) {
-            float r[8];
-            rr[j].get(r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] = as_stored(R{}, h[j][i] + r[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] = as_stored(R{}, h[j][i]);
-        }
+    for (int j = 0; j < kV; ++j) {
+        norm_sum(rx[j], rr[j], a.res != nullptr, h[j], s);
         const int c = tid + j * nthr;
         if (a.res_out && c < nch) store8(R{}, a.res_out, base + 8 * c, h[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const double d = (double)h[j][i];
-            s = fma(d, d, s);
-        }
     }
-    s = wave_sum_f64(s);
-    if (nthr > kWave) {
-        if ((tid & 63) == 0) part[tid >> 6] = s;
-        __syncthreads();
-        s = 0.0;
-        for (int w = 0; w < nthr / kWave; ++w) s += part[w];
-    }
+    s = block_sum_f64(s, part);
     const double r = 1.0 / sqrt(s / (double)a.H + (double)a.eps);
     if (a.rstd && tid == 0) a.rstd[row] = (float)r;
-    const float rf = (float)r;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < kV; ++j) {
         const int c = tid + j * nthr;
-        float w[8], y[8];
+        float w[8];
         rw[j].get(w);
-        if (a.q_kind == MOE_Q_NONE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = h[j][i] * rf * w[i];
-        } else {
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const double n = (double)h[j][i] * r;
-                const float v = sticky_f32(n * (double)w[i]);
-                q[i] = a.q_kind == MOE_Q_OUTPUT ? v : sticky_f32(n);
-                y[i] = v;
-            }
-            uint32_t sc;
-            const uint2 codes = mx_encode(q, &sc);   // H % 32 == 0: the four lanes of a block are in or out together
-            if (c < nch) {
-                *reinterpret_cast<uint2 *>(a.codes + base + 8 * c) = codes;
-                if ((c & 3) == 0) a.scales[(base >> 5) + (c >> 2)] = (uint8_t)sc;
-            }
-        }
-        if (a.y && c < nch) store8(Bf16{}, a.y, base + 8 * c, y);
+        norm_out(a, base, c, c < nch, h[j], w, r);
     }
 }
 
-template <int V, typename X>
-hipError_t norm_v(const NormArgs &a, int waves, hipStream_t st) {
-    const dim3 g(a.T), b(kWave * waves);
-    if (a.res_dtype == MOE_OUT_F32)
-        MOE_LAUNCH("rms_norm", (rms_norm<V, X, float>), g, b, 0, st, a);
+// The same for rows of over kNormRow elements, which are read twice.  The
+// second pass takes h from residual_out where the first wrote it (it may have
+// replaced the residual or x there).
+template <typename X, typename R>
+__global__ __launch_bounds__(kWave *kNormMaxWaves) void rms_norm_wide(NormArgs a) {
+    __shared__ double part[kNormMaxWaves];
+    const size_t row = blockIdx.x;
+    const int tid = threadIdx.x, nthr = blockDim.x, nch = a.H / 8;
+    const size_t base = row * (size_t)a.H;
+    double s = 0.0;
+    auto chunk = [&](int c, float *h) {
+        Raw8<X> rx;
+        Raw8<R> rr;
+        rr.zero();
+        rx.load(a.x, base + 8 * c);
+        if (a.res) rr.load(a.res, base + 8 * c);
+        norm_sum(rx, rr, a.res != nullptr, h, s);
+    };
+#pragma unroll 2
+    for (int c = tid; c < nch; c += nthr) {
+        float h[8];
+        chunk(c, h);
+        if (a.res_out) store8(R{}, a.res_out, base + 8 * c, h);
+    }
+    s = block_sum_f64(s, part);
+    const double r = 1.0 / sqrt(s / (double)a.H + (double)a.eps);
+    if (a.rstd && tid == 0) a.rstd[row] = (float)r;
+    for (int c0 = 0; c0 < nch; c0 += nthr) {   // every lane takes part: four of them share a block of 32
+        const int c = c0 + tid, cc = c < nch ? c : nch - 1;
+        float h[8], w[8];
+        if (a.res_out) {
+            Raw8<R> rr;
+            rr.load(a.res_out, base + 8 * cc);
+            rr.get(h);
+        } else {
+            chunk(cc, h);
+        }
+        Raw8<float> rw;
+        rw.load(a.weight, 8 * cc);
+        rw.get(w);
+        norm_out(a, base, c, c < nch, h, w, r);
+    }
+}
+
+template <typename X, typename R>
+void norm_launch(const NormArgs &a, hipStream_t st) {
+    const dim3 g(a.T), b(kWave * row_waves(a.H));
+    if (a.H <= kNormRow)
+        MOE_LAUNCH("rms_norm", (rms_norm<X, R>), g, b, 0, st, a);
     else
-        MOE_LAUNCH("rms_norm", (rms_norm<V, X, Bf16>), g, b, 0, st, a);
-    return hipGetLastError();
+        MOE_LAUNCH("rms_norm", (rms_norm_wide<X, R>), g, b, 0, st, a);
 }
 
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st) {
-    const RowShape r = row_shape(a.H);
-    const bool xf = a.x_dtype == MOE_OUT_F32;
-    if (r.v == 2) return xf ? norm_v<2, float>(a, r.waves, st) : norm_v<2, Bf16>(a, r.waves, st);
-    return xf ? norm_v<8, float>(a, r.waves, st) : norm_v<8, Bf16>(a, r.waves, st);
+    const bool xf = a.x_dtype == MOE_OUT_F32, rf = a.res_dtype == MOE_OUT_F32;
+    if (xf && rf)
+        norm_launch<float, float>(a, st);
+    else if (xf)
+        norm_launch<float, Bf16>(a, st);
+    else if (rf)
+        norm_launch<Bf16, float>(a, st);
+    else
+        norm_launch<Bf16, Bf16>(a, st);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -196,11 +266,13 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// Blocks (partial rows of dweight).  A constant, so that the order of the sums
-// depends on the sizes alone.
-constexpr int kNormBwdBlocks = 512;
-
-int norm_bwd_blocks(int T) { return T < kNormBwdBlocks ? T : kNormBwdBlocks; }
+// Blocks (partial rows of dweight): about 2048 waves, 512 blocks at least.  By
+// the sizes alone, so that the order of the sums depends on nothing else.
+int norm_bwd_blocks(int T, int H) {
+    const int waves = row_waves(H);
+    const int n = waves < 4 ? 2048 / waves : 512;
+    return T < n ? T : n;
+}
 
 template <typename S>
 __device__ __forceinline__ void load_src(Raw8<S> &r, const NormBwdArgs &a, size_t i) {
@@ -210,13 +282,32 @@ __device__ __forceinline__ void load_src(Raw8<S> &r, const NormBwdArgs &a, size_
         r.load(a.h, i);
 }
 
-template <int V, typename DY, typename S, typename DR, typename DX>
-__global__ __launch_bounds__(1024) void rms_norm_backward(NormBwdArgs a, float *__restrict__ dwpart) {
-    __shared__ float part[2][kNormMaxWaves];
-    const int tid = threadIdx.x, nthr = blockDim.x, nch = a.H / 8, nw = nthr / kWave;
-    float w[V][8], dw[V][8];
+// dy (times the weight) and n of eight elements, with their part of dweight
+// and of the row's sum of g n.
+template <typename DY, typename S>
+__device__ __forceinline__ void bwd_terms(const Raw8<DY> &ry, const Raw8<S> &rs, float r, const float *w, float *g,
+                                          float *n, float *dw, float &s) {
+    ry.get(g);
+    rs.get(n);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (!__is_same(S, Mx8)) n[i] *= r;
+        dw[i] = fmaf(g[i], n[i], dw[i]);
+        g[i] *= w[i];
+        s = fmaf(g[i], n[i], s);
+    }
+}
+
+// At most MW waves per row.  Rows of up to 4096 elements (MW = 4) have the
+// registers for two rows: the block's next token is loaded while the current
+// one is worked on.
+template <int MW, typename DY, typename S, typename DR, typename DX>
+__global__ __launch_bounds__(kWave *MW) void rms_norm_backward(NormBwdArgs a, float *__restrict__ dwpart) {
+    __shared__ float part[2][MW];
+    const int tid = threadIdx.x, nthr = blockDim.x, nch = a.H / 8, nw = nthr / kWave;
+    float w[kV][8], dw[kV][8];
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
         const int c = tid + j * nthr;
         Raw8<float> rw;
         if (c < nch)
@@ -227,167 +318,245 @@ __global__ __launch_bounds__(1024) void rms_norm_backward(NormBwdArgs a, float *
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
     }
-    int par = 0;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
-        const size_t base = (size_t)t * a.H;
-        if (a.mask && a.mask[t] == 0) {   // the same for the whole block
-            const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    struct Row {
+        Raw8<DY> y[kV];
+        Raw8<S> s[kV];
+        Raw8<DR> d[kV];
+        float r;
+        bool on;
+    };
+    auto load = [&](Row &q, int t) __attribute__((always_inline)) {
+        q.on = t < a.T && !(a.mask && a.mask[t] == 0);   // the same for the whole block
+        if (!q.on) return;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = tid + j * nthr;
-                if (a.dx && c < nch) store8(DX{}, a.dx, base + 8 * c, z);
-            }
-            par ^= 1;   // no barrier was passed: keep the parity
-            continue;
-        }
-        Raw8<DY> ry[V];
-        Raw8<S> rs[V];
-        Raw8<DR> rd[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < kV; ++j) {
             const int c = tid + j * nthr;
+            const size_t at = (size_t)t * a.H + 8 * c;
+            q.d[j].zero();
             if (c < nch) {
-                ry[j].load(a.dy, base + 8 * c);
-                load_src<S>(rs[j], a, base + 8 * c);
-                if (a.dres) rd[j].load(a.dres, base + 8 * c);
+                q.y[j].load(a.dy, at);
+                load_src<S>(q.s[j], a, at);
+                if (a.dres) q.d[j].load(a.dres, at);
             } else {
-                ry[j].zero();
-                rs[j].zero();
-                rd[j].zero();
+                q.y[j].zero();
+                q.s[j].zero();
             }
         }
-        const float r = a.rstd[t];
-        float dy[V][8], n[V][8];
-        float s = 0.f;
+        q.r = a.rstd[t];
+    };
+    int par = 0;
+    auto work = [&](const Row &q, int t) __attribute__((always_inline)) {
+        float g[kV][8], n[kV][8], o[8], s = 0.f, m = 0.f;
+        if (q.on) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            ry[j].get(dy[j]);
-            rs[j].get(n[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (!__is_same(S, Mx8)) n[j][i] *= r;
-                dw[j][i] = fmaf(dy[j][i], n[j][i], dw[j][i]);
-                dy[j][i] *= w[j][i];
-                s = fmaf(dy[j][i], n[j][i], s);
+            for (int j = 0; j < kV; ++j) bwd_terms(q.y[j], q.s[j], q.r, w[j], g[j], n[j], dw[j], s);
+        }
+        if (a.dx == nullptr) return;
+        if (q.on) {
+            s = wave_sum(s);
+            if (nw > 1) {
+                // two slots in turn: a slot is written again only after the
+                // barrier of the row between, which its readers have reached
+                if ((tid & 63) == 0) part[par][tid >> 6] = s;
+                __syncthreads();
+                s = 0.f;
+                for (int k = 0; k < nw; ++k) s += part[par][k];
+                par ^= 1;
             }
+            m = s / (float)a.H;
         }
-        if (a.dx == nullptr) {
-            par ^= 1;
-            continue;
-        }
-        s = wave_sum(s);
-        if (nw > 1) {
-            // two slots in turn: a slot is written again only after the
-            // barrier of the row between, which its readers have reached
-            if ((tid & 63) == 0) part[par][tid >> 6] = s;
-            __syncthreads();
-            s = 0.f;
-            for (int q = 0; q < nw; ++q) s += part[par][q];
-        }
-        const float m = s / (float)a.H;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < kV; ++j) {
             const int c = tid + j * nthr;
-            float d[8], o[8];
-            if (a.dres)
-                rd[j].get(d);
-            else {
+            float d[8];
+            q.d[j].get(d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = 0.f;
+            for (int i = 0; i < 8; ++i) o[i] = q.on ? fmaf(q.r, g[j][i] - n[j][i] * m, d[i]) : 0.f;
+            if (c < nch) store8(DX{}, a.dx, (size_t)t * a.H + 8 * c, o);
+        }
+    };
+    const int step = gridDim.x;
+    if constexpr (MW == 4) {
+        Row r0, r1;
+        load(r0, blockIdx.x);
+        for (int t = blockIdx.x; t < a.T; t += 2 * step) {
+            load(r1, t + step);
+            work(r0, t);
+            if (t + step < a.T) {
+                load(r0, t + 2 * step);
+                work(r1, t + step);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(r, dy[j][i] - n[j][i] * m, d[i]);
-            if (c < nch) store8(DX{}, a.dx, base + 8 * c, o);
+        }
+    } else {
+        for (int t = blockIdx.x; t < a.T; t += step) {
+            Row r;
+            load(r, t);
+            work(r, t);
         }
     }
     if (a.dweight) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < kV; ++j) {
             const int c = tid + j * nthr;
             if (c < nch) store8(float{}, dwpart, (size_t)blockIdx.x * a.H + 8 * c, dw[j]);
         }
     }
 }
 
-// Column sums: block = 64 columns, sixteen waves take the rows w, w + 16, ...,
-// eight in flight each.
+// Rows of over kNormRow elements.  dx: a block per token, which reads its row
+// once for the sum and once for the result.
+template <typename DY, typename S, typename DR, typename DX>
+__global__ __launch_bounds__(kWave *kNormMaxWaves) void rms_norm_backward_wide(NormBwdArgs a) {
+    __shared__ float part[kNormMaxWaves];
+    const int tid = threadIdx.x, nthr = blockDim.x, nch = a.H / 8, t = blockIdx.x;
+    const size_t base = (size_t)t * a.H;
+    const bool on = !(a.mask && a.mask[t] == 0);
+    const float r = on ? a.rstd[t] : 0.f;
+    float s = 0.f, none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    auto chunk = [&](int c, float *g, float *n) {
+        Raw8<DY> ry;
+        Raw8<S> rs;
+        Raw8<float> rw;
+        float w[8];
+        ry.load(a.dy, base + 8 * c);
+        load_src<S>(rs, a, base + 8 * c);
+        rw.load(a.weight, 8 * c);
+        rw.get(w);
+        bwd_terms(ry, rs, r, w, g, n, none, s);
+    };
+    float g[8], n[8];
+    if (on) {
+#pragma unroll 2
+        for (int c = tid; c < nch; c += nthr) chunk(c, g, n);
+    }
+    s = wave_sum(s);
+    if ((tid & 63) == 0) part[tid >> 6] = s;
+    __syncthreads();
+    float sum = 0.f;
+    for (int k = 0; k < nthr / kWave; ++k) sum += part[k];
+    const float m = sum / (float)a.H;
+#pragma unroll 2
+    for (int c = tid; c < nch; c += nthr) {
+        float d[8], o[8];
+        Raw8<DR> rd;
+        rd.zero();
+        if (on && a.dres) rd.load(a.dres, base + 8 * c);
+        rd.get(d);
+        if (on) chunk(c, g, n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = on ? fmaf(r, g[i] - n[i] * m, d[i]) : 0.f;
+        store8(DX{}, a.dx, base + 8 * c, o);
+    }
+}
+
+// dweight's partial rows for the same: block (x: 2048 columns, y: partial row)
+// takes the tokens y, y + partial rows, ...  The columns' tokens are read
+// before dx is written (dx may replace dy or h in place).
+template <typename DY, typename S>
+__global__ __launch_bounds__(256) void norm_dweight_wide(NormBwdArgs a, float *__restrict__ dwpart) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.H / 8) return;
+    const float one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, g[8], n[8], s = 0.f;
+    for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
+        if (a.mask && a.mask[t] == 0) continue;
+        Raw8<DY> ry;
+        Raw8<S> rs;
+        ry.load(a.dy, (size_t)t * a.H + 8 * c);
+        load_src<S>(rs, a, (size_t)t * a.H + 8 * c);
+        bwd_terms(ry, rs, a.rstd[t], one, g, n, dw, s);
+    }
+    store8(float{}, dwpart, (size_t)blockIdx.y * a.H + 8 * c, dw);
+}
+
+// Column sums: block = 16 columns, 64 chains of rows (r, r + 64, ...; a wave has
+// four of them side by side), eight rows of a chain in flight.
 __global__ __launch_bounds__(1024) void column_sum(const float *__restrict__ part, int R, int C,
                                                    float *__restrict__ out) {
-    __shared__ float lds[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane, cc = c < C ? c : C - 1;
+    __shared__ float lds[16][16];
+    const int tid = threadIdx.x, wave = tid >> 6, col = tid & 15, chain = tid >> 4;
+    const int c = blockIdx.x * 16 + col, cc = c < C ? c : C - 1;
     float s = 0.f;
-    for (int r = wave; r < R; r += 128) {
+    for (int r = chain; r < R; r += 512) {
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = part[(size_t)(r + 16 * i < R ? r + 16 * i : r) * C + cc];
+        for (int i = 0; i < 8; ++i) v[i] = part[(size_t)(r + 64 * i < R ? r + 64 * i : r) * C + cc];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += r + 16 * i < R ? v[i] : 0.f;
+        for (int i = 0; i < 8; ++i) s += r + 64 * i < R ? v[i] : 0.f;
     }
-    lds[wave][lane] = s;
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if ((tid & 63) < 16) lds[wave][col] = s;
     __syncthreads();
-    if (wave == 0 && c < C) {
+    if (tid < 16 && c < C) {
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            v[i] = (lds[4 * i][lane] + lds[4 * i + 1][lane]) + (lds[4 * i + 2][lane] + lds[4 * i + 3][lane]);
+            v[i] = (lds[4 * i][col] + lds[4 * i + 1][col]) + (lds[4 * i + 2][col] + lds[4 * i + 3][col]);
         out[c] = (v[0] + v[1]) + (v[2] + v[3]);
     }
 }
 
-template <int V, typename DY, typename S, typename DR>
-void bwd_dx(const NormBwdArgs &a, int waves, float *part, hipStream_t st) {
-    const dim3 g(norm_bwd_blocks(a.T)), b(kWave * waves);
+template <typename DY, typename S, typename DR, typename DX>
+void bwd_launch(const NormBwdArgs &a, float *part, hipStream_t st) {
+    const int waves = row_waves(a.H), n = norm_bwd_blocks(a.T, a.H);
+    const dim3 b(kWave * waves);
+    if (a.H > kNormRow) {
+        if (a.dweight)
+            MOE_LAUNCH("norm_dweight_wide", (norm_dweight_wide<DY, S>), dim3((a.H / 8 + 255) / 256, n), dim3(256), 0, st,
+                       a, part);
+        if (a.dx)
+            MOE_LAUNCH("rms_norm_backward", (rms_norm_backward_wide<DY, S, DR, DX>), dim3(a.T), b, 0, st, a);
+    } else if (waves <= 4) {
+        MOE_LAUNCH("rms_norm_backward", (rms_norm_backward<4, DY, S, DR, DX>), dim3(n), b, 0, st, a, part);
+    } else {
+        MOE_LAUNCH("rms_norm_backward", (rms_norm_backward<kNormMaxWaves, DY, S, DR, DX>), dim3(n), b, 0, st, a, part);
+    }
+}
+template <typename DY, typename S, typename DR>
+void bwd_dx(const NormBwdArgs &a, float *part, hipStream_t st) {
     if (a.dx_dtype == MOE_OUT_F32)
-        MOE_LAUNCH("rms_norm_backward", (rms_norm_backward<V, DY, S, DR, float>), g, b, 0, st, a, part);
+        bwd_launch<DY, S, DR, float>(a, part, st);
     else
-        MOE_LAUNCH("rms_norm_backward", (rms_norm_backward<V, DY, S, DR, Bf16>), g, b, 0, st, a, part);
+        bwd_launch<DY, S, DR, Bf16>(a, part, st);
 }
-template <int V, typename DY, typename S>
-void bwd_dr(const NormBwdArgs &a, int waves, float *part, hipStream_t st) {
+template <typename DY, typename S>
+void bwd_dr(const NormBwdArgs &a, float *part, hipStream_t st) {
     if (a.dres_dtype == MOE_OUT_F32)
-        bwd_dx<V, DY, S, float>(a, waves, part, st);
+        bwd_dx<DY, S, float>(a, part, st);
     else
-        bwd_dx<V, DY, S, Bf16>(a, waves, part, st);
+        bwd_dx<DY, S, Bf16>(a, part, st);
 }
-template <int V, typename DY>
-void bwd_src(const NormBwdArgs &a, int waves, float *part, hipStream_t st) {
+template <typename DY>
+void bwd_src(const NormBwdArgs &a, float *part, hipStream_t st) {
     if (a.h == nullptr)
-        bwd_dr<V, DY, Mx8>(a, waves, part, st);
+        bwd_dr<DY, Mx8>(a, part, st);
     else if (a.h_dtype == MOE_OUT_F32)
-        bwd_dr<V, DY, float>(a, waves, part, st);
+        bwd_dr<DY, float>(a, part, st);
     else
-        bwd_dr<V, DY, Bf16>(a, waves, part, st);
-}
-template <int V>
-void bwd_dy(const NormBwdArgs &a, int waves, float *part, hipStream_t st) {
-    if (a.dy_dtype == MOE_OUT_F32)
-        bwd_src<V, float>(a, waves, part, st);
-    else
-        bwd_src<V, Bf16>(a, waves, part, st);
+        bwd_dr<DY, Bf16>(a, part, st);
 }
 
 }  // namespace
 
 hipError_t launch_column_sum(const char *name, const float *part, int R, int C, float *out, hipStream_t st) {
-    MOE_LAUNCH(name, column_sum, dim3((C + 63) / 64), dim3(1024), 0, st, part, R, C, out);
+    MOE_LAUNCH(name, column_sum, dim3((C + 15) / 16), dim3(1024), 0, st, part, R, C, out);
     return hipGetLastError();
 }
 
-size_t norm_bwd_ws_bytes(int T, int H) { return WsLayout::up((size_t)norm_bwd_blocks(T) * H * 4); }
+size_t norm_bwd_ws_bytes(int T, int H) { return WsLayout::up((size_t)norm_bwd_blocks(T, H) * H * 4); }
 
 hipError_t launch_rms_norm_backward(const NormBwdArgs &a, char *ws, hipStream_t st) {
-    const RowShape r = row_shape(a.H);
     float *part = reinterpret_cast<float *>(ws);
     if (a.T > 0) {
-        if (r.v == 2)
-            bwd_dy<2>(a, r.waves, part, st);
+        if (a.dy_dtype == MOE_OUT_F32)
+            bwd_src<float>(a, part, st);
         else
-            bwd_dy<8>(a, r.waves, part, st);
+            bwd_src<Bf16>(a, part, st);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.dweight) return launch_column_sum("dweight_sum", part, norm_bwd_blocks(a.T), a.H, a.dweight, st);
+    if (a.dweight) return launch_column_sum("dweight_sum", part, norm_bwd_blocks(a.T, a.H), a.H, a.dweight, st);
     return hipSuccess;
 }
 

@@ -71,7 +71,7 @@ struct RouteBwdArgs {
 size_t route_bwd_ws_bytes(int T, int H, int E);
 hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st);
 
-// out[c] = sum over r of part[r][c] in sixteen interleaved chains of rows
+// out[c] = sum over r of part[r][c] in 64 interleaved chains of rows
 // (a fixed order for a given R); part [R][C].  R = 0 writes zeros.
 hipError_t launch_column_sum(const char *name, const float *part, int R, int C, float *out, hipStream_t st);
 
@@ -99,54 +99,57 @@ template <typename T>
 struct Raw8;
 template <>
 struct Raw8<float> {
-    float4 a, b;
+    f32x4 a, b;
     __device__ __forceinline__ void load(const void *p, size_t i) {
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        const f32x4 *q = reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + i);
         a = q[0];
         b = q[1];
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
     __device__ __forceinline__ void get(float *v) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
     }
 };
 template <>
 struct Raw8<Bf16> {
-    uint4 a;
+    u32x4 a;
     __device__ __forceinline__ void load(const void *p, size_t i) {
-        a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+        a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
     }
-    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void zero() { a = u32x4{0u, 0u, 0u, 0u}; }
     __device__ __forceinline__ void get(float *v) const {
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            v[2 * i] = __uint_as_float(a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
         }
     }
 };
 template <>
 struct Raw8<Mx8> {
-    uint2 a;
-    uint32_t s;
+    uint32_t lo, hi, s;
     __device__ __forceinline__ void load2(const uint8_t *codes, const uint8_t *scales, size_t i) {
-        a = *reinterpret_cast<const uint2 *>(codes + i);
+        const uint2 a = *reinterpret_cast<const uint2 *>(codes + i);
+        lo = a.x;
+        hi = a.y;
         s = scales[i >> 5];
     }
     __device__ __forceinline__ void zero() {
-        a = make_uint2(0u, 0u);
+        lo = hi = 0u;
         s = 127;
     }
     // the values the codes stand for (exact: four significant bits)
     __device__ __forceinline__ void get(float *v) const {
         typedef float f2 __attribute__((ext_vector_type(2)));
         const float sc = e8m0_to_f32(s);
-        const f2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.x, false);
-        const f2 p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.x, true);
-        const f2 p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.y, false);
-        const f2 p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a.y, true);
+        const f2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, false);
+        const f2 p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, true);
+        const f2 p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, false);
+        const f2 p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, true);
         v[0] = p0[0] * sc; v[1] = p0[1] * sc; v[2] = p1[0] * sc; v[3] = p1[1] * sc;
         v[4] = p2[0] * sc; v[5] = p2[1] * sc; v[6] = p3[0] * sc; v[7] = p3[1] * sc;
     }

@@ -77,7 +77,8 @@ class Norm:
 
 
 @pytest.mark.parametrize("kind", [moe.MOE_Q_NONE, moe.MOE_Q_OUTPUT, moe.MOE_Q_NORMALIZED])
-@pytest.mark.parametrize("T,H", [(1, 4096), (3, 128), (5, 1152), (2, 2176), (7, 640), (2, 16384), (1, 16512), (2, 65536)])
+@pytest.mark.parametrize("T,H", [(1, 4096), (3, 128), (5, 1152), (2, 2176), (7, 640), (9, 1024), (2, 16384), (1, 16512),
+                                 (2, 65536)])
 @pytest.mark.parametrize("xt,rt", [(B16, B16), (F32, F32), (F32, B16), (B16, F32)])
 def test_norm(T, H, xt, rt, kind):
     c = Norm(T, H, xt, rt, kind, seed=T + H)
