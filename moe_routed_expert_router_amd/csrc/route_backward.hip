@@ -395,6 +395,8 @@ __device__ __forceinline__ void wait_vmem_to() {
     asm volatile("" ::: "memory");
 }
 
+constexpr int kStage = 48 * kUnit;   // an LDS stage of either product (three of them)
+
 // Unit i of the n consecutive units at src to dst + i units, by this wave.
 __device__ __forceinline__ void fill_unit(const uint8_t *src, int n, uint8_t *dst, int i) {
     lds_fill<16>(buffer_rsrc(src, n * kUnit), i * kUnit + 16 * (threadIdx.x & 63), dst + i * kUnit);
@@ -422,19 +424,18 @@ struct DxTiles {
 // way while a tile is finished and stored.  LDS is a ring of three 48 KB
 // stages, filled two steps ahead.
 template <int NP, typename DX>
-__global__ __launch_bounds__(512) void route_dx(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp,
-                                                const int32_t *__restrict__ tscale, const int32_t *__restrict__ hscale,
-                                                int T, int H, int EC, int TG, DxTiles tiles, void *__restrict__ dx) {
+__device__ __forceinline__ void dx_block(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp,
+                                         const int32_t *__restrict__ tscale, const int32_t *__restrict__ hscale, int T,
+                                         int H, int EC, int TG, const DxTiles &tiles, void *__restrict__ dx, int block,
+                                         int blocks, uint8_t *st0, uint8_t *st1, uint8_t *st2) {
     constexpr int KC = 4 / NP;   // 16-expert chunks per step: KC NP = 4 units per group
     constexpr int kOpA = 8 * 4 * kUnit, kOpB = 4 * 4 * kUnit;
+    static_assert(kOpA + kOpB <= kStage, "stage size");
     constexpr int kFills = 6;    // per wave and step
-    __shared__ __align__(1024) uint8_t st0[kOpA + kOpB];
-    __shared__ __align__(1024) uint8_t st1[kOpA + kOpB];
-    __shared__ __align__(1024) uint8_t st2[kOpA + kOpB];
     const int total = tiles.HT * tiles.TT, per = (total + 7) / 8;
-    const int xcd = blockIdx.x & 7, slots = gridDim.x >> 3;
+    const int xcd = block & 7, slots = blocks >> 3;
     const int last = (xcd + 1) * per < total ? (xcd + 1) * per : total;
-    const int first = xcd * per + (blockIdx.x >> 3);
+    const int first = xcd * per + (block >> 3);
     if (first >= last) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int HG = H / 32, S = EC / KC;
@@ -664,22 +665,21 @@ __device__ __forceinline__ int x_slot(int s) { return 16 * (s ^ ((s >> 3) & 1));
 // its stage.
 // out: the split's partial [E][H], or dWr itself with one split.
 template <bool MX>
-__global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *__restrict__ dzt,
-                                                 const uint32_t *__restrict__ valid, int EG, int steps, int splits,
-                                                 float *__restrict__ out) {
+__device__ __forceinline__ void dwr_block(const RouteBwdArgs &a, const uint8_t *__restrict__ dzt,
+                                          const uint32_t *__restrict__ valid, int EG, int steps, int splits,
+                                          float *__restrict__ out, int block, uint8_t *st0, uint8_t *st1,
+                                          uint8_t *st2) {
     constexpr int kA = 4 * 2 * 3 * kUnit, kB = 8 * 2 * kUnit;
+    static_assert(kA + kB <= kStage, "stage size");
     constexpr int kLoads = 3 + (MX ? 16 : 8);   // per wave and step: dz units, x rows
-    __shared__ __align__(1024) uint8_t st0[kA + kB];
-    __shared__ __align__(1024) uint8_t st1[kA + kB];
-    __shared__ __align__(1024) uint8_t st2[kA + kB];
     const int H = a.H, E = a.E;
     const int net = (E + kTileE - 1) / kTileE;
     const int nht = (H + kTileH - 1) / kTileH;
     // the expert tiles of one (split, hidden tile) are consecutive on one XCD
     // (they read the same x), and an XCD stays with few splits (the same dz)
     const int total = net * nht * splits, per = (total + 7) / 8;
-    const int idx = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || idx >= total) return;
+    const int idx = (block & 7) * per + (block >> 3);
+    if ((block >> 3) >= per || idx >= total) return;
     const int et = idx % net, ht = (idx / net) % nht, sp = idx / (net * nht);
     const int per_split = (steps + splits - 1) / splits;
     const int s0 = sp * per_split, s1 = s0 + per_split < steps ? s0 + per_split : steps;
@@ -819,6 +819,30 @@ __global__ __launch_bounds__(512) void route_dwr(RouteBwdArgs a, const uint8_t *
     }
 }
 
+// Both products in one launch, a block per compute unit at a time: blocks [0,
+// n_dwr) have dWr, the following n_dx dx (both multiples of 8, so that a
+// block's number modulo 8 is its XCD).  The blocks of dx start as those of dWr
+// end: neither waits for the other's last round.
+template <int NP, typename DX, bool MX>
+__global__ __launch_bounds__(512) void route_products(RouteBwdArgs a, const uint8_t *__restrict__ dza,
+                                                      const uint8_t *__restrict__ dzt, const uint8_t *__restrict__ wrp,
+                                                      const int32_t *__restrict__ tscale,
+                                                      const int32_t *__restrict__ hscale,
+                                                      const uint32_t *__restrict__ valid, int TG, int EC, int EG,
+                                                      int splits, float *__restrict__ dwr, int n_dwr, DxTiles tiles,
+                                                      int n_dx) {
+    // three separate arrays, used with fixed roles per unrolled step, so the
+    // compiler can tell a fill's destination from the stage being read
+    __shared__ __align__(1024) uint8_t st0[kStage];
+    __shared__ __align__(1024) uint8_t st1[kStage];
+    __shared__ __align__(1024) uint8_t st2[kStage];
+    const int b = blockIdx.x;
+    if (b < n_dwr)
+        dwr_block<MX>(a, dzt, valid, EG, TG, splits, dwr, b, st0, st1, st2);
+    else
+        dx_block<NP, DX>(dza, wrp, tscale, hscale, a.T, a.H, EC, TG, tiles, a.dx, b - n_dwr, n_dx, st0, st1, st2);
+}
+
 // The sums over blocks.  Blocks [0, n_dwr): dWr from the splits' partials, in
 // split order, times the checkpoint's column weight; the others: 64 columns of
 // db each from the token groups' parts, four interleaved chains.
@@ -870,10 +894,9 @@ __global__ __launch_bounds__(256) void route_zero(float *p, size_t n) {
 // products: dz as fp32 rows [T][E8] (E rounded up to 8, zeros past E), and
 // both products straight from the fp32 operands on the 32x32x2 fp32 MFMA, in
 // one launch whose blocks have one of three roles (dx, dWr, db).
-// H 4096, E 384: 12 against 31 us at 32 and 48 tokens, 31 against 35 at 128
-// (fp32 dx: 31 against 44), 44 against 38 at 192; H 1024, E 64: 24 against 26
-// us at 128.
-constexpr int kFewTokens = 128;
+// H 4096, E 384: 24 against 29 us at 96 tokens, 31 against 29 at 128 (12 at 32);
+// H 1024, E 64: 19 against 20 at 96, 24 against 20 at 128.
+constexpr int kFewTokens = 96;
 
 template <int NPL>
 __global__ __launch_bounds__(256) void route_dz_rows(RouteBwdArgs a, float *__restrict__ dz, int E8) {
@@ -1061,17 +1084,23 @@ void launch_operands(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStrea
 #undef MOE_OPS
 }
 
-template <int NP, typename DX>
-void launch_dx(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
+template <int NP, typename DX, bool MX>
+void launch_products(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
+    const uint8_t *u = reinterpret_cast<const uint8_t *>(ws);
     DxTiles t;
     t.HT = (a.H + kTileH - 1) / kTileH;
     t.TT = (a.T + kTileT - 1) / kTileT;
     t.hper = (t.HT + 7) / 8;
-    const int per = (t.HT * t.TT + 7) / 8, slots = per < kCus / 8 ? per : kCus / 8;
-    MOE_LAUNCH("route_dx", (route_dx<NP, DX>), dim3(8 * slots), dim3(512), 0, st,
-               reinterpret_cast<const uint8_t *>(ws + w.dza), reinterpret_cast<const uint8_t *>(ws + w.wrp),
-               reinterpret_cast<const int32_t *>(ws + w.tscale), reinterpret_cast<const int32_t *>(ws + w.hscale), a.T,
-               a.H, w.ec, w.tg, t, a.dx);
+    const int per = (t.HT * t.TT + 7) / 8;
+    const int n_dx = a.dx ? 8 * (per < kCus / 8 ? per : kCus / 8) : 0;
+    const int tiles = ((a.E + kTileE - 1) / kTileE) * t.HT * w.splits;
+    const int n_dwr = a.dwr ? 8 * ((tiles + 7) / 8) : 0;
+    float *dwr = w.splits > 1 ? reinterpret_cast<float *>(ws + w.dwp) : a.dwr;
+    if (n_dx + n_dwr > 0)
+        MOE_LAUNCH("route_products", (route_products<NP, DX, MX>), dim3(n_dwr + n_dx), dim3(512), 0, st, a, u + w.dza,
+                   u + w.dzt, u + w.wrp, reinterpret_cast<const int32_t *>(ws + w.tscale),
+                   reinterpret_cast<const int32_t *>(ws + w.hscale), reinterpret_cast<const uint32_t *>(ws + w.valid),
+                   w.tg, w.ec, w.eg, w.splits, dwr, n_dwr, t, n_dx);
 }
 
 }  // namespace
@@ -1095,24 +1124,16 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st
         launch_operands<2>(a, w, ws, st);
     else
         launch_operands<1>(a, w, ws, st);
-    if (a.dx) {
-        if (terms == 2)
-            launch_dx<2, float>(a, w, ws, st);
-        else
-            launch_dx<1, Bf16>(a, w, ws, st);
-    }
+    const bool mx = a.x == nullptr;
+    if (terms == 2 && mx)
+        launch_products<2, float, true>(a, w, ws, st);
+    else if (terms == 2)
+        launch_products<2, float, false>(a, w, ws, st);
+    else if (mx)
+        launch_products<1, Bf16, true>(a, w, ws, st);
+    else
+        launch_products<1, Bf16, false>(a, w, ws, st);
     float *part = reinterpret_cast<float *>(ws + w.dwp);
-    if (a.dwr) {
-        const uint8_t *dzt = reinterpret_cast<const uint8_t *>(ws + w.dzt);
-        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ws + w.valid);
-        float *out = w.splits > 1 ? part : a.dwr;
-        const int total = ((a.E + kTileE - 1) / kTileE) * ((a.H + kTileH - 1) / kTileH) * w.splits;
-        const dim3 g(8 * ((total + 7) / 8));
-        if (a.x == nullptr)
-            MOE_LAUNCH("route_dwr", route_dwr<true>, g, dim3(512), 0, st, a, dzt, valid, w.eg, w.tg, w.splits, out);
-        else
-            MOE_LAUNCH("route_dwr", route_dwr<false>, g, dim3(512), 0, st, a, dzt, valid, w.eg, w.tg, w.splits, out);
-    }
     const size_t n4 = ne / 4;
     const int n_dwr = a.dwr && w.splits > 1 ? (int)((n4 + 255) / 256) : 0, n_db = a.db ? (a.E + 63) / 64 : 0;
     if (n_dwr + n_db > 0)

@@ -393,18 +393,18 @@ class Route:
         wx, ww, wb = ot.route_backward(dz, np.where(keep[:, None], self.xv, 0), f64(self.wr), m)
         W, X, Z = np.abs(f64(self.wr)), np.abs(np.where(keep[:, None], self.xv, 0)), np.abs(dz)
         Ep = -(-E // 32) * 32
-        # dx above 128 tokens: fp16 terms of factors scaled per row (dz) and
+        # dx above 96 tokens: fp16 terms of factors scaled per row (dz) and
         # column (Wr) to a largest magnitude of 2^14 or more.  A term leaves
         # 2^-11 of the value, two leave 2^-22, and what is under half of fp16's
         # least step, 2^-25, i.e. 2^-39 of the largest.  bf16 out: one term,
         # |zw - z1 w1| <= (2 2^-11 + 2^-22) |z||w|.  fp32 out: hi hi + hi lo +
-        # lo hi: 2 2^-22 left of the factors and lo lo <= 2^-22.  Up to 128 tokens
+        # lo hi: 2 2^-22 left of the factors and lo lo <= 2^-22.  Up to 96 tokens
         # the products are fp32's.  The accumulation rounds once for each of
         # nprod Ep additions (2 U: a matrix core may truncate).
         one = self.dx.dtype == B16
         split, nprod = (2.001 * 2.0 ** -11, 1) if one else (3 * 2.0 ** -22, 3)
         floor = 2.0 ** -38 * (Z.max(1, keepdims=True) * W.sum(0) + Z.sum(1, keepdims=True) * W.max(0))
-        if T <= 128:
+        if T <= 96:
             split, nprod, floor = U, 1, (Ep + 32) * 2.0 ** -150
         b = err @ W + (split + 2 * U * nprod * (Ep + 32)) * (Z @ W) + floor
         # and half the least step that the stored type has: 2^-133 (bf16),
@@ -417,7 +417,7 @@ class Route:
 
 @pytest.mark.parametrize("src,renorm,dxt", [("x", True, B16), ("x", False, F32), ("q_norm", True, F32), ("q_out", False, B16)])
 @pytest.mark.parametrize("T,H,E,k", [(1, 128, 8, 2), (4, 256, 8, 2), (33, 384, 40, 3), (130, 128, 257, 8), (64, 640, 1, 1),
-                                     (300, 1024, 130, 4), (40, 256, 1024, 32), (128, 256, 33, 2), (129, 384, 40, 3),
+                                     (300, 1024, 130, 4), (40, 256, 1024, 32), (96, 256, 33, 2), (97, 384, 40, 3), (128, 256, 64, 2),
                                      (140, 256, 1024, 32), (161, 896, 385, 6), (256, 128, 8, 2)])
 def test_route_backward(T, H, E, k, src, renorm, dxt):
     c = Route(T, H, E, k, src, renorm, mask=T > 4, dxt=dxt, seed=T)
