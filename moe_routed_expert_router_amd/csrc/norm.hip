@@ -266,12 +266,14 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// Blocks (partial rows of dweight): about 2048 waves, 512 blocks at least.  By
-// the sizes alone, so that the order of the sums depends on nothing else.
+// Blocks (partial rows of dweight): about 2048 waves, 512 blocks at least, each
+// with the same number of tokens but the last.  By the sizes alone, so that
+// the order of the sums depends on nothing else.
 int norm_bwd_blocks(int T, int H) {
     const int waves = row_waves(H);
-    const int n = waves < 4 ? 2048 / waves : 512;
-    return T < n ? T : n;
+    const int most = waves < 4 ? 2048 / waves : 512;
+    const int per = (T + most - 1) / most;
+    return per > 0 ? (T + per - 1) / per : 0;
 }
 
 template <typename S>

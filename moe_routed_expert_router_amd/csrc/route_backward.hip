@@ -33,6 +33,10 @@ namespace moe {
 
 namespace {
 
+// For lambdas that are called from several places: a call would keep the
+// accumulators in memory.
+#define MOE_INLINE __attribute__((always_inline))
+
 constexpr int kUnit = 1024;   // bytes of an operand unit
 constexpr int kDzTok = 32;    // tokens per block of route_dz
 
@@ -381,10 +385,6 @@ __device__ __forceinline__ void even_end() {
     lds_barrier();   // the fills stay in flight
     __builtin_amdgcn_sched_barrier(0);
 }
-
-// For lambdas that are called from several places: a call would keep the
-// accumulators in memory.
-#define MOE_INLINE __attribute__((always_inline))
 
 // Wait until at most N of this wave's global operations are outstanding.
 template <int N>
@@ -894,8 +894,10 @@ __global__ __launch_bounds__(256) void route_zero(float *p, size_t n) {
 // products: dz as fp32 rows [T][E8] (E rounded up to 8, zeros past E), and
 // both products straight from the fp32 operands on the 32x32x2 fp32 MFMA, in
 // one launch whose blocks have one of three roles (dx, dWr, db).
-// H 4096, E 384: 24 against 29 us at 96 tokens, 31 against 29 at 128 (12 at 32);
-// H 1024, E 64: 19 against 20 at 96, 24 against 20 at 128.
+// At 96 against 97 tokens (the first that takes the other path): H 4096, E 384
+// 21 against 25 us (fp32 dx from a checkpoint 25 against 29), H 1024, E 64 16
+// against 20; this path grows with the tokens (11 us at 32), the other does
+// not (26 at 128, 31 at 256).
 constexpr int kFewTokens = 96;
 
 template <int NPL>
@@ -985,33 +987,56 @@ __device__ void few_dwr(const RouteBwdArgs &a, const float *__restrict__ dz, int
     f32x16 acc[2];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
-    for (int t0 = 0; t0 < a.T; t0 += 16) {
-        float d[8], x0[8], x1[8];
+    // sixteen tokens at a time, the next sixteen on their way
+    struct Batch {
+        float d[8];
+        uint32_t v[8], s[8];
+    };
+    auto load = [&](Batch &q, int t0) MOE_INLINE {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int t = t0 + 2 * i + half;
             const bool in = t < a.T && !(a.mask && a.mask[t] == 0);
             const int tc = in ? t : 0;
-            d[i] = in ? dz[(size_t)tc * E8 + ec] : 0.f;
+            const float d = dz[(size_t)tc * E8 + ec];
             const size_t at = (size_t)tc * a.H + h;
+            uint32_t v, sc = 127;
             if constexpr (MX) {
-                typedef float f2 __attribute__((ext_vector_type(2)));
-                const uint32_t v = *reinterpret_cast<const uint16_t *>(a.codes + at);
-                const float sc = e8m0_to_f32(a.scales[at >> 5]);
-                const f2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)v, false);
-                x0[i] = in ? f[0] * sc : 0.f;
-                x1[i] = in ? f[1] * sc : 0.f;
+                v = *reinterpret_cast<const uint16_t *>(a.codes + at);
+                sc = a.scales[at >> 5];
             } else {
-                const uint32_t v = *reinterpret_cast<const uint32_t *>(a.x + at);
-                x0[i] = in ? __uint_as_float(v << 16) : 0.f;
-                x1[i] = in ? __uint_as_float(v & 0xffff0000u) : 0.f;
+                v = *reinterpret_cast<const uint32_t *>(a.x + at);
             }
+            q.d[i] = in ? d : 0.f;
+            q.v[i] = in ? v : 0u;
+            q.s[i] = in ? sc : 127u;
         }
+    };
+    auto products = [&](const Batch &q) MOE_INLINE {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            acc[0] = mfma32x32x2(d[i], x0[i], acc[0]);
-            acc[1] = mfma32x32x2(d[i], x1[i], acc[1]);
+            float x0, x1;
+            if constexpr (MX) {
+                typedef float f2 __attribute__((ext_vector_type(2)));
+                const float sc = e8m0_to_f32(q.s[i]);
+                const f2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.v[i], false);
+                x0 = f[0] * sc;
+                x1 = f[1] * sc;
+            } else {
+                x0 = __uint_as_float(q.v[i] << 16);
+                x1 = __uint_as_float(q.v[i] & 0xffff0000u);
+            }
+            acc[0] = mfma32x32x2(q.d[i], x0, acc[0]);
+            acc[1] = mfma32x32x2(q.d[i], x1, acc[1]);
         }
+    };
+    Batch b0, b1;
+    load(b0, 0);
+    for (int t0 = 0; t0 < a.T; t0 += 32) {
+        load(b1, t0 + 16);
+        products(b0);
+        if (t0 + 32 < a.T) load(b0, t0 + 32);
+        if (t0 + 16 < a.T) products(b1);
     }
     float w0 = 1.f, w1 = 1.f;
     if (MX && a.q_weight) {
