@@ -253,17 +253,19 @@ public:
             dev_ = -1;
         }
     }
-    void in(const void *p, size_t bytes, size_t align, const char *name) { add(p, bytes, align, name, false); }
-    void out(const void *p, size_t bytes, size_t align, const char *name) { add(p, bytes, align, name, true); }
-    // `out` may replace `in` in place (checked by the caller: same type)
-    void in_place(const void *out, const void *in) {
-        if (n_pairs_ < kMaxPairs) pairs_[n_pairs_++] = {out, in};
+    // Both return the argument's number, for in_place.
+    int in(const void *p, size_t bytes, size_t align, const char *name) { return add(p, bytes, align, name, false); }
+    int out(const void *p, size_t bytes, size_t align, const char *name) { return add(p, bytes, align, name, true); }
+    // argument `out` may replace argument `in` in place (-1: not there; the
+    // caller has checked that their types are the same)
+    void in_place(int out, int in) {
+        if (out >= 0 && in >= 0) pairs_[n_pairs_++] = {out, in};
     }
     moe_status status(void *stream) {
         if (st_ != MOE_OK) return st_;
         for (int i = 0; i < n_; ++i)
             for (int j = 0; j < n_; ++j)
-                if (b_[i].out && i != j && (j > i || !b_[j].out) && overlap(b_[i], b_[j]) && !allowed(b_[i].p, b_[j].p))
+                if (b_[i].out && i != j && (j > i || !b_[j].out) && overlap(b_[i], b_[j]) && !allowed(i, j))
                     return fail(MOE_ERR_INVALID_ARG, "%s and %s overlap", b_[i].name, b_[j].name);
         if (stream) {
             hipDevice_t d = -1;
@@ -289,28 +291,29 @@ private:
         const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
         return x < y + b.bytes && y < x + a.bytes;
     }
-    bool allowed(const void *p, const void *q) const {
-        if (p != q) return false;
+    bool allowed(int out, int in) const {
+        if (b_[out].p != b_[in].p) return false;
         for (int i = 0; i < n_pairs_; ++i)
-            if (pairs_[i].out == p && pairs_[i].in == q) return true;
+            if (pairs_[i].out == out && pairs_[i].in == in) return true;
         return false;
     }
-    void add(const void *p, size_t bytes, size_t align, const char *name, bool out) {
-        if (st_ != MOE_OK) return;
+    int add(const void *p, size_t bytes, size_t align, const char *name, bool out) {
+        if (st_ != MOE_OK) return -1;
         int device = -1;
-        if ((st_ = check_ptr(p, bytes, align, name, &device)) != MOE_OK) return;
+        if ((st_ = check_ptr(p, bytes, align, name, &device)) != MOE_OK) return -1;
         if (dev_ < 0)
             st_ = fail(MOE_ERR_HIP, "no usable current device");
         else if (device >= 0 && device != dev_)
             st_ = fail(MOE_ERR_INVALID_ARG, "%s is memory of device %d, the current one is %d", name, device, dev_);
-        else
-            b_[n_++] = {p, bytes, out, name};
+        if (st_ != MOE_OK) return -1;
+        b_[n_] = {p, bytes, out, name};
+        return n_++;
     }
     int dev_ = -1, n_ = 0, n_pairs_ = 0;
     moe_status st_ = MOE_OK;
     Buf b_[kMax];
     struct Pair {
-        const void *out, *in;
+        int out, in;
     } pairs_[kMaxPairs];
 };
 
@@ -768,19 +771,19 @@ moe_status moe_rms_norm(const moe_shape *s, int32_t T, int32_t x_dtype, const vo
     if (T == 0) return ok();
     const size_t n = (size_t)T * s->hidden;
     ArgCheck c;
-    c.in(x, n * elem_bytes(x_dtype), 16, "x");
-    if (residual) c.in(residual, n * elem_bytes(residual_dtype), 16, "residual");
+    const int ix = c.in(x, n * elem_bytes(x_dtype), 16, "x");
+    const int ires = residual ? c.in(residual, n * elem_bytes(residual_dtype), 16, "residual") : -1;
     c.in(weight, (size_t)s->hidden * 4, 16, "weight");
-    if (residual_out) c.out(residual_out, n * elem_bytes(residual_dtype), 16, "residual_out");
-    if (y) c.out(y, n * 2, 16, "y");
+    const int iro = residual_out ? c.out(residual_out, n * elem_bytes(residual_dtype), 16, "residual_out") : -1;
+    const int iy = y ? c.out(y, n * 2, 16, "y") : -1;
     if (q_kind != MOE_Q_NONE) {
         c.out(q_codes, n, 8, "q_codes");
         c.out(q_scales, n / 32, 4, "q_scales");
     }
     if (rstd) c.out(rstd, (size_t)T * 4, 4, "rstd");
-    c.in_place(residual_out, residual);
-    if (x_dtype == residual_dtype) c.in_place(residual_out, x);
-    if (x_dtype == MOE_OUT_BF16) c.in_place(y, x);
+    c.in_place(iro, ires);
+    if (x_dtype == residual_dtype) c.in_place(iro, ix);
+    if (x_dtype == MOE_OUT_BF16) c.in_place(iy, ix);
     TRY(c.status(stream));
     moe::NormArgs a{};
     a.T = T;
@@ -820,10 +823,11 @@ moe_status moe_rms_norm_backward(const moe_shape *s, int32_t T, int32_t dy_dtype
     if (T > 0) TRY(check_train_ws(need, ws_bytes));
     ArgCheck c;
     if (T > 0) {
-        c.in(dy, n * elem_bytes(dy_dtype), 16, "dy");
-        if (dresidual) c.in(dresidual, n * elem_bytes(dresidual_dtype), 16, "dresidual");
+        const int idy = c.in(dy, n * elem_bytes(dy_dtype), 16, "dy");
+        const int idr = dresidual ? c.in(dresidual, n * elem_bytes(dresidual_dtype), 16, "dresidual") : -1;
+        int ih = -1;
         if (h) {
-            c.in(h, n * elem_bytes(h_dtype), 16, "h");
+            ih = c.in(h, n * elem_bytes(h_dtype), 16, "h");
         } else {
             c.in(q_codes, n, 8, "q_codes");
             c.in(q_scales, n / 32, 4, "q_scales");
@@ -831,11 +835,11 @@ moe_status moe_rms_norm_backward(const moe_shape *s, int32_t T, int32_t dy_dtype
         c.in(rstd, (size_t)T * 4, 4, "rstd");
         c.in(weight, (size_t)s->hidden * 4, 16, "weight");
         if (token_mask) c.in(token_mask, (size_t)T, 1, "token_mask");
-        if (dx) c.out(dx, n * elem_bytes(dx_dtype), 16, "dx");
+        const int idx = dx ? c.out(dx, n * elem_bytes(dx_dtype), 16, "dx") : -1;
         c.out(ws, need, 256, "ws");
-        if (dx_dtype == dy_dtype) c.in_place(dx, dy);
-        if (dresidual && dx_dtype == dresidual_dtype) c.in_place(dx, dresidual);
-        if (h && dx_dtype == h_dtype) c.in_place(dx, h);
+        if (dx_dtype == dy_dtype) c.in_place(idx, idy);
+        if (dx_dtype == dresidual_dtype) c.in_place(idx, idr);
+        if (dx_dtype == h_dtype) c.in_place(idx, ih);
     }
     if (dweight) c.out(dweight, (size_t)s->hidden * 4, 16, "dweight");
     TRY(c.status(stream));
@@ -922,14 +926,13 @@ moe_status moe_balance_loss_backward(const moe_shape *s, int32_t T, const float 
     if (T == 0) return ok();
     const size_t E = s->n_experts;
     ArgCheck c;
-    c.in(logits, (size_t)T * E * 4, 4, "logits");
+    const int iz = c.in(logits, (size_t)T * E * 4, 4, "logits");
     if (token_mask) c.in(token_mask, (size_t)T, 1, "token_mask");
     if (seq_offsets) c.in(seq_offsets, ((size_t)n_seq + 1) * 4, 4, "seq_offsets");
     if (dloss) c.in(dloss, 4, 4, "dloss");
     c.in(counts, (size_t)n_seq * E * 4, 4, "counts");
     c.in(n_valid, ((size_t)n_seq + 1) * 4, 4, "n_valid");
-    c.out(dlogits, (size_t)T * E * 4, 4, "dlogits");
-    c.in_place(dlogits, logits);
+    c.in_place(c.out(dlogits, (size_t)T * E * 4, 4, "dlogits"), iz);
     TRY(c.status(stream));
     TRY(hip_status(moe::launch_balance_loss_backward(
                        balance_args(s, T, logits, nullptr, token_mask, seq_offsets, n_seq, alpha), dloss, counts,

@@ -304,6 +304,39 @@ def test_balance_bad_offsets_stay_inside():
         assert torch.all(o["counts"] >= 0) and torch.all(torch.isfinite(o["dlogits"]))
 
 
+@pytest.mark.parametrize("T", [20, 200])
+def test_balance_nonfinite_rows(T):
+    """NaN and +inf reach the loss, their sequence's means and their own rows;
+    -inf is a probability of 0 and a row of nothing else counts as a token."""
+    E, k = 70, 3
+    s = moe.shape(128, 128, E, k)
+    for bad in (float("nan"), float("inf")):
+        z, ids = routing(4, T, E, k)
+        z[3, 5] = bad
+        off = torch.tensor([0, T // 2, T], dtype=torch.int32, device="cuda")
+        for o in (None, off):
+            r = balance(s, z, ids, None, o, 0.1)
+            torch.cuda.synchronize()
+            assert torch.isnan(r["loss"]).all() and torch.isnan(r["prob_mean"][0]).all()
+            assert torch.isnan(r["dlogits"][3]).all()
+            assert torch.isfinite(r["dlogits"][4:]).all() and torch.isfinite(r["prob_mean"][1:]).all()
+            assert r["counts"].sum().item() == T * k
+    z = torch.full((T, E), float("-inf"), device="cuda")
+    r = balance(s, z, ids, None, None, 0.1)
+    torch.cuda.synchronize()
+    assert r["loss"].item() == 0 and torch.all(r["dlogits"] == 0) and r["n_valid"].tolist() == [T, 1]
+
+
+def test_balance_in_place():
+    s = moe.shape(128, 128, 40, 3)
+    z, ids = routing(2, 300, 40, 3)
+    o = balance(s, z, ids, None, None, 0.1)
+    dz = z.clone()
+    moe.moe_balance_loss_backward(s, dz, None, None, 0.1, None, o["counts"], o["n_valid"], dz)
+    torch.cuda.synchronize()
+    assert torch.equal(dz, o["dlogits"])
+
+
 def test_balance_empty():
     s = moe.shape(128, 128, 8, 2)
     z, ids = torch.empty((0, 8), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda")
@@ -525,6 +558,67 @@ def test_empty_batch_writes_zero_sums():
     assert torch.all(dw == 0) and torch.all(dwr == 0) and torch.all(db == 0)
 
 
+# ------------------------------ the largest sizes ---------------------------
+def test_elements_past_32_bits():
+    """2^20 tokens: the tensors' last elements are past 2^32 (x, dx) and their
+    bytes past it (logits); the last rows and the sums over all of them."""
+    T, H, E, k = 1 << 20, 4224, 8, 2
+    s = moe.shape(H, 128, E, k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((T, H), dtype=B16, device="cuda").normal_(generator=g)
+    w = 1 + rnd(1, (H,), 0.2)
+    y = torch.empty_like(x)
+    codes = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    sc = torch.empty((T, H // 32), dtype=torch.uint8, device="cuda")
+    r = torch.empty(T, device="cuda")
+    moe.moe_rms_norm(s, x, None, w, EPS, None, y, moe.MOE_Q_NORMALIZED, codes, sc, r)
+    rows = [0, 1, T // 2 + 1, T - 2, T - 1]
+    h, wr, n, wy = ot.rms_norm(f64(x[rows]), None, f64(w), float(np.float32(EPS)), False, False)
+    close(y[rows], wy, np.abs(wy) * (UB + 4 * U))
+    c0, s0 = ot.mx8_encode(n)
+    assert np.array_equal(codes[rows].cpu().numpy(), c0) and np.array_equal(sc[rows].cpu().numpy(), s0)
+    # backward of the norm, dx over y's memory
+    dw = torch.empty(H, device="cuda")
+    ws = new_ws(s, T)
+    moe.moe_rms_norm_backward(s, x, None, None, codes, sc, r, w, None, y, dw, ws)
+    dx, _ = ot.rms_norm_backward(f64(x[rows]), None, ot.mx8_decode(c0, s0), f64(r[rows]), f64(w))
+    close(y[rows], dx, np.abs(dx) * UB + 1e-4)
+    # the router's backward: every token has the same two picks' gradient
+    dz = torch.full((T, E), 0.0, device="cuda")
+    dz[:, 3] = 1.0
+    dz[T - 1, 5] = 2.0
+    wrt = rnd(2, (E, H), 0.1)
+    dwr, db = torch.empty((E, H), device="cuda"), torch.empty(E, device="cuda")
+    moe.moe_route_backward(s, x, None, None, None, wrt, True, None, None, None, None, dz, None, y, dwr, db, ws)
+    torch.cuda.synchronize()
+    want = f64(dz[rows]) @ f64(wrt)
+    close(y[rows], want, np.abs(want) * UB + 3e-3 * (np.abs(f64(dz[rows])) @ np.abs(f64(wrt))))
+    total = sum(x[i:i + 65536].double().sum(0) for i in range(0, T, 65536)).cpu().numpy()
+    # 2^20 values of order 1 in fp32: a random walk of roundings of sums of
+    # order 2^10, 2^15 additions in a chain each
+    assert np.max(np.abs(f64(dwr[3]) - total)) < 0.05
+    assert np.array_equal(f64(dwr[5]), 2 * f64(x[T - 1])) and torch.all(dwr[[0, 1, 2, 4, 6, 7]] == 0)
+    assert db.tolist() == [0, 0, 0, float(T), 0, 2, 0, 0]
+    del x, y, codes, sc, ws, dz
+    # logits of 4 GB
+    E = 1024
+    s = moe.shape(128, 128, E, 1)
+    z = torch.empty((T, E), device="cuda").normal_(generator=g)
+    ids = torch.full((T, 1), 7, dtype=torch.int32, device="cuda")
+    o = balance(s, z, ids, None, None, 1.0)
+    torch.cuda.synchronize()
+    assert o["counts"][0, 7].item() == T and o["counts"].sum().item() == T
+    p = sum(torch.softmax(z[i:i + 65536].double(), 1).sum(0) for i in range(0, T, 65536)) / T
+    assert torch.max(torch.abs(o["prob_mean"][0].double() - p) / p).item() < 1e-5
+    assert abs(o["loss"].item() - E * p[7].item()) < 1e-5 * E * p[7].item()
+    t = T - 1
+    pr = torch.softmax(z[t].double(), 0)
+    a = torch.zeros(E, dtype=torch.float64, device="cuda")
+    a[7] = E / T
+    want = pr * (a - (pr * a).sum())
+    assert torch.max(torch.abs(o["dlogits"][t].double() - want)).item() < 1e-5 * a[7].item()
+
+
 # ------------------------------ in use together -----------------------------
 class Chain:
     """norm -> route -> balance loss, then back: balance, router, norm (from
@@ -687,6 +781,9 @@ def test_refusals():
         moe.moe_rms_norm(s, c.x, c.res, c.w, EPS, c.ro.float(), c.y)
     torch.cuda.synchronize()
     assert torch.all(c.ro == 7) and torch.all(c.y == 7)
+
+    # in place twice: y and residual_out both over x
+    refuse(arg, moe.moe_rms_norm, s, c.x, c.res, c.w, EPS, c.x, c.x)
 
     dy, r, dw = rnd(1, (T, H)), torch.ones(T, device="cuda"), torch.full((H,), 7.0, device="cuda")
     ws = new_ws(s, T, 3)
