@@ -13,7 +13,7 @@
 #include <mutex>
 
 #include "kernels.hpp"
-#include "train/train.hpp"
+#include "train.h"
 
 namespace {
 

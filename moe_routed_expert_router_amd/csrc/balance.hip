@@ -10,7 +10,7 @@
 // (the counts are piecewise constant: no gradient through them).  A row whose
 // logits are all -inf has p = 0.  Both directions read z once; the backward
 // computes the softmax again instead of storing T x E probabilities.
-#include "train/train.hpp"
+#include "train.h"
 
 namespace moe {
 

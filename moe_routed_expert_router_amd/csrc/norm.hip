@@ -10,7 +10,7 @@
 //
 // Both directions are bound by HBM traffic: every input is read once into
 // registers and every output written once.
-#include "train/train.hpp"
+#include "train.h"
 
 namespace moe {
 

@@ -27,7 +27,7 @@
 // of the contraction, lane l's eight (row l % 32, contraction 8 (l / 32) ..
 // +7) at byte 16 l.  A unit goes to LDS as one linear copy and to registers
 // as one conflict-free 16-byte read per lane.
-#include "train/train.hpp"
+#include "train.h"
 
 namespace moe {
 

@@ -1,10 +1,11 @@
 // Launchers and shared device code of the norm and of the router's training
-// side (norm.hip, balance.hip, route_backward.hip).  In a folder of its own:
-// the layer's forward kernels do not depend on it.
+// side (norm.hip, balance.hip, route_backward.hip).  A .h file, not one of the
+// .hpp headers that every kernel shares: the counter summaries of the layer's
+// forward kernels are tied to those, and these do not include this one.
 #pragma once
 
-#include "../device_util.hpp"
-#include "../kernels.hpp"
+#include "device_util.hpp"
+#include "kernels.hpp"
 
 namespace moe {
 
