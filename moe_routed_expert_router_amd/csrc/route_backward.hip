@@ -402,16 +402,30 @@ __device__ __forceinline__ void fill_unit(const uint8_t *src, int n, uint8_t *ds
     lds_fill<16>(buffer_rsrc(src, n * kUnit), i * kUnit + 16 * (threadIdx.x & 63), dst + i * kUnit);
 }
 
-// Tiles of dx in the order an XCD takes them: hidden tiles in groups of `hper`
-// (an eighth of them), token tiles outside, so that the blocks of one XCD share
-// few rows of Wr and all of them reuse the dz rows they bring into its L2.
+// Division by a number that the host knows: m = floor((2^32 - 1) / d) is at
+// most one quotient low for every n < 2^32.
+struct Divisor {
+    uint32_t d, m;
+    explicit Divisor(int n) : d(n), m(0xffffffffu / (uint32_t)n) {}
+    __device__ __forceinline__ int divide(int n, int &rest) const {
+        const int q = (int)__umulhi((uint32_t)n, m), r = n - q * (int)d;
+        rest = r >= (int)d ? r - (int)d : r;
+        return r >= (int)d ? q + 1 : q;
+    }
+};
+
+// Tiles of dx in the order an XCD takes them: hidden tiles in groups of an
+// eighth of them, token tiles outside, so that the blocks of one XCD share few
+// rows of Wr and all of them reuse the dz rows they bring into its L2.
 struct DxTiles {
-    int HT, TT, hper;
+    int HT, TT;
+    Divisor group, whole, rest;   // tiles of a group; hidden tiles of a whole group and of the last one
+    DxTiles(int ht, int tt, int per) : HT(ht), TT(tt), group(tt * per), whole(per), rest((ht - 1) % per + 1) {}
     __device__ __forceinline__ void at(int idx, int &ht, int &tt) const {
-        const int grp = idx / (TT * hper), in = idx - grp * TT * hper;
-        const int width = HT - grp * hper < hper ? HT - grp * hper : hper;
-        tt = in / width;
-        ht = grp * hper + in - tt * width;
+        int in;
+        const int first = group.divide(idx, in) * (int)whole.d;
+        tt = (HT - first < (int)whole.d ? rest : whole).divide(in, ht);
+        ht += first;
     }
 };
 
@@ -427,7 +441,7 @@ template <int NP, typename DX>
 __device__ __forceinline__ void dx_block(const uint8_t *__restrict__ dza, const uint8_t *__restrict__ wrp,
                                          const int32_t *__restrict__ tscale, const int32_t *__restrict__ hscale, int T,
                                          int H, int EC, int TG, const DxTiles &tiles, void *__restrict__ dx, int block,
-                                         int blocks, uint8_t *st0, uint8_t *st1, uint8_t *st2) {
+                                         int blocks, uint8_t *st0, uint8_t *st1, uint8_t *st2, int32_t *rows_ts) {
     constexpr int KC = 4 / NP;   // 16-expert chunks per step: KC NP = 4 units per group
     constexpr int kOpA = 8 * 4 * kUnit, kOpB = 4 * 4 * kUnit;
     static_assert(kOpA + kOpB <= kStage, "stage size");
@@ -508,6 +522,14 @@ __device__ __forceinline__ void dx_block(const uint8_t *__restrict__ dza, const 
         const __amdgpu_buffer_rsrc_t out = buffer_rsrc(static_cast<uint8_t *>(dx) + (size_t)(rows > 0 ? t0 : 0) * H * kSize,
                                                        rows > 0 ? (uint32_t)rows * H * kSize : 0u);
         const uint32_t lane_off = h < H ? ((uint32_t)(4 * half) * H + h) * kSize : 0x80000000u;
+        // a wave's own 64 entries of LDS turn "token per lane" into "tokens per row"
+        rows_ts[64 * wave + lane] = -ts;
+        int4 tr[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                tr[i][q] = *reinterpret_cast<const int4 *>(&rows_ts[64 * wave + 32 * i + 8 * q + 4 * half]);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -515,10 +537,9 @@ __device__ __forceinline__ void dx_block(const uint8_t *__restrict__ dza, const 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 32 * i + 8 * q + r;   // + 4 in the upper half
-                    const int lo = __builtin_amdgcn_readlane(ts, row), hi = __builtin_amdgcn_readlane(ts, row + 4);
-                    const int tr = half ? hi : lo;
-                    const float v0 = ldexpf(acc[i][0][4 * q + r], -tr - hs.x);
-                    const float v1 = ldexpf(acc[i][1][4 * q + r], -tr - hs.y);
+                    const int t = r == 0 ? tr[i][q].x : r == 1 ? tr[i][q].y : r == 2 ? tr[i][q].z : tr[i][q].w;
+                    const float v0 = ldexpf(acc[i][0][4 * q + r], t - hs.x);
+                    const float v1 = ldexpf(acc[i][1][4 * q + r], t - hs.y);
                     const uint32_t off = lane_off + (uint32_t)row * H * kSize;
                     if constexpr (__is_same(DX, float)) {
                         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -836,11 +857,13 @@ __global__ __launch_bounds__(512) void route_products(RouteBwdArgs a, const uint
     __shared__ __align__(1024) uint8_t st0[kStage];
     __shared__ __align__(1024) uint8_t st1[kStage];
     __shared__ __align__(1024) uint8_t st2[kStage];
+    __shared__ __align__(16) int32_t rows_ts[8 * 64];
     const int b = blockIdx.x;
     if (b < n_dwr)
         dwr_block<MX>(a, dzt, valid, EG, TG, splits, dwr, b, st0, st1, st2);
     else
-        dx_block<NP, DX>(dza, wrp, tscale, hscale, a.T, a.H, EC, TG, tiles, a.dx, b - n_dwr, n_dx, st0, st1, st2);
+        dx_block<NP, DX>(dza, wrp, tscale, hscale, a.T, a.H, EC, TG, tiles, a.dx, b - n_dwr, n_dx, st0, st1, st2,
+                         rows_ts);
 }
 
 // The sums over blocks.  Blocks [0, n_dwr): dWr from the splits' partials, in
@@ -1112,13 +1135,11 @@ void launch_operands(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStrea
 template <int NP, typename DX, bool MX>
 void launch_products(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
     const uint8_t *u = reinterpret_cast<const uint8_t *>(ws);
-    DxTiles t;
-    t.HT = (a.H + kTileH - 1) / kTileH;
-    t.TT = (a.T + kTileT - 1) / kTileT;
-    t.hper = (t.HT + 7) / 8;
-    const int per = (t.HT * t.TT + 7) / 8;
+    const int HT = (a.H + kTileH - 1) / kTileH;
+    const DxTiles t(HT, (a.T + kTileT - 1) / kTileT, (HT + 7) / 8);
+    const int per = (HT * t.TT + 7) / 8;
     const int n_dx = a.dx ? 8 * (per < kCus / 8 ? per : kCus / 8) : 0;
-    const int tiles = ((a.E + kTileE - 1) / kTileE) * t.HT * w.splits;
+    const int tiles = ((a.E + kTileE - 1) / kTileE) * HT * w.splits;
     const int n_dwr = a.dwr ? 8 * ((tiles + 7) / 8) : 0;
     float *dwr = w.splits > 1 ? reinterpret_cast<float *>(ws + w.dwp) : a.dwr;
     if (n_dx + n_dwr > 0)
