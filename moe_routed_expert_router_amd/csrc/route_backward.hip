@@ -627,40 +627,61 @@ __device__ __forceinline__ void dx_block(const uint8_t *__restrict__ dza, const 
 
 // ----------------------------------- dWr -----------------------------------
 // Tokens of one thread's piece of a step: two hidden columns x eight tokens,
-// as two bf16 per dword (x) or two codes and their scale (checkpoint).  The
-// eight rows are one buffer; a row that takes no part (past the end, or
-// masked) and a column past H get an offset outside it and read as zeros,
-// whatever is stored.
+// as two bf16 per dword (x) or two codes (checkpoint).  The eight rows are one
+// buffer; a row that takes no part (past the end, or masked) and a column past
+// H get an offset outside it and read as zeros, whatever is stored.
+// Checkpoint scales: the 16 lanes of a DPP row have the 32 columns of one scale,
+// so lane i (and i + 8) of the row loads the scale of token i, and a row
+// broadcast hands it on: one byte load per step instead of eight.
 constexpr uint32_t kOutside = 0x40000000u;   // elements; eight rows have at most 2^19
+
+// Lane I of each row of 16 lanes.
+template <int I>
+__device__ __forceinline__ float row_lane(float v) {
+    const int b = __float_as_int(v);
+    return __int_as_float(__builtin_amdgcn_update_dpp(b, b, 0x150 | I, 0xf, 0xf, true));   // row_newbcast
+}
+
 template <bool MX>
 struct XPiece {
     uint32_t v[8];
-    uint32_t s[MX ? 8 : 1];
-    // row t0 + i (t0 uniform), bit i of `valid` for it; column h (kOutside: none)
-    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, uint32_t h, int i) {
-        const bool in = (valid >> i) & 1u;
+    uint32_t s;
+    // rows t0 .. t0 + 7 (t0 uniform), bit i of `valid` for row i; column h (kOutside: none)
+    __device__ __forceinline__ void load(const RouteBwdArgs &a, int t0, uint32_t valid, uint32_t h) {
         const size_t row = (size_t)t0 * a.H;
-        const uint32_t at = in ? (uint32_t)i * a.H + h : kOutside;
-        if constexpr (MX) {
-            v[i] = __builtin_amdgcn_raw_buffer_load_b16(buffer_rsrc(a.codes + row, 8 * a.H), at, 0, 0);
-            s[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(a.scales + (row >> 5), a.H >> 2), at >> 5, 0, 0);
-        } else {
-            v[i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(a.x + row, 16 * a.H), 2 * at, 0, 0);
+        auto at = [&](int i) { return (valid >> i) & 1u ? (uint32_t)i * a.H + h : kOutside; };
+        if constexpr (MX)
+            s = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(a.scales + (row >> 5), a.H >> 2),
+                                                    at(threadIdx.x & 7) >> 5, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (MX)
+                v[i] = __builtin_amdgcn_raw_buffer_load_b16(buffer_rsrc(a.codes + row, 8 * a.H), at(i), 0, 0);
+            else
+                v[i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(a.x + row, 16 * a.H), 2 * at(i), 0, 0);
         }
     }
     // the eight tokens of column h (lo) and h + 1 (hi) as 16-byte pieces
     __device__ __forceinline__ void pieces(uint4 &lo, uint4 &hi) {
         uint32_t d[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (MX) {
+        if constexpr (MX) {
+            const float sc = e8m0_to_f32(s);
+            auto bf16s = [](uint32_t codes, float scale) {
                 typedef float f2 __attribute__((ext_vector_type(2)));
-                const f2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[i], false);
-                const float sc = e8m0_to_f32(s[i]);
-                d[i] = bf16x2_bits(f[0] * sc, f[1] * sc);
-            } else {
-                d[i] = v[i];
-            }
+                const f2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
+                return bf16x2_bits(f[0] * scale, f[1] * scale);
+            };
+            d[0] = bf16s(v[0], row_lane<0>(sc));
+            d[1] = bf16s(v[1], row_lane<1>(sc));
+            d[2] = bf16s(v[2], row_lane<2>(sc));
+            d[3] = bf16s(v[3], row_lane<3>(sc));
+            d[4] = bf16s(v[4], row_lane<4>(sc));
+            d[5] = bf16s(v[5], row_lane<5>(sc));
+            d[6] = bf16s(v[6], row_lane<6>(sc));
+            d[7] = bf16s(v[7], row_lane<7>(sc));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = v[i];
         }
         uint32_t l[4], u[4];
 #pragma unroll
@@ -692,7 +713,7 @@ __device__ __forceinline__ void dwr_block(const RouteBwdArgs &a, const uint8_t *
                                           uint8_t *st2) {
     constexpr int kA = 4 * 2 * 3 * kUnit, kB = 8 * 2 * kUnit;
     static_assert(kA + kB <= kStage, "stage size");
-    constexpr int kLoads = 3 + (MX ? 16 : 8);   // per wave and step: dz units, x rows
+    constexpr int kLoads = 3 + (MX ? 9 : 8);   // per wave and step: dz units, x rows
     const int H = a.H, E = a.E;
     const int net = (E + kTileE - 1) / kTileE;
     const int nht = (H + kTileH - 1) / kTileH;
@@ -740,8 +761,7 @@ __device__ __forceinline__ void dwr_block(const RouteBwdArgs &a, const uint8_t *
     auto load_x = [&](XPiece<MX> &x, int s) MOE_INLINE {
         const int n = s < s1 ? s : s1 - 1;
         const uint32_t ok = tokens(n);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x.load(a, kStepK * n + 8 * oct, ok, h, i);
+        x.load(a, kStepK * n + 8 * oct, ok, h);
     };
     auto fill_a = [&](uint8_t *st, int s) MOE_INLINE {
         const int n = s < s1 ? s : s1 - 1;
