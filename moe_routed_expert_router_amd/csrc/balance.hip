@@ -10,6 +10,11 @@
 // (the counts are piecewise constant: no gradient through them).  A row whose
 // logits are all -inf has p = 0.  Both directions read z once; the backward
 // computes the softmax again instead of storing T x E probabilities.
+//
+// 8192 tokens of 384 experts, one group (12.6 MB of logits): sums 6.7 us,
+// reduction 5.7, backward 7.1 (12.6 MB read, 12.6 written).  The three launches
+// bound it, not the bytes (a kernel of this chain that does nothing costs 4 to
+// 5 us back to back); the logits come from the memory-side cache.
 #include "train.h"
 
 namespace moe {
@@ -134,7 +139,8 @@ __device__ __forceinline__ float sum16(const float (&v)[kBalWaves]) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Sums of one chunk: probabilities in registers over the wave's tokens (two at
+// Sums of one chunk (a block of 16 waves for 32 tokens, so that 8192 tokens are
+// a block per compute unit): probabilities in registers over the wave's tokens (two at
 // a time, so that one's loads and reductions run beside the other's), picks in
 // an LDS histogram (integers: the order of the additions is immaterial).
 // ONE: the chunk is the whole batch and its only group; the block finishes the
@@ -325,7 +331,9 @@ __global__ __launch_bounds__(kBalThreads) void balance_reduce(BalanceArgs a, int
     }
 }
 
-// One wave per token at a time; a block takes `rows` consecutive tokens.
+// One wave per token at a time; a block takes `rows` consecutive tokens.  (Two
+// tokens at a time in a wave, as in the sums, was slower: 20.1 against 19.5 us for
+// both directions at 8192 x 384.)
 template <int NPL>
 __global__ __launch_bounds__(256) void balance_backward(BalanceArgs a, int rows, const float *__restrict__ dloss,
                                                         const int32_t *__restrict__ counts,

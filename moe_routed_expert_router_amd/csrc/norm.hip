@@ -9,7 +9,11 @@
 //             dweight = sum over tokens of dy n
 //
 // Both directions are bound by HBM traffic: every input is read once into
-// registers and every output written once.
+// registers and every output written once.  Measured with inputs that change
+// from call to call, where a 1 GiB copy runs at 5.0 TB/s: 8192 tokens of 4096,
+// bf16 with residual, y and checkpoint (303 MB) 60 us = 5.0 TB/s; its backward
+// with dweight (268 MB) 56 us = 4.8 TB/s.  Small calls are bound by the launch:
+// one token 3.9 us, 32 tokens with the 8-bit output 5.2 us.
 #include "train.h"
 
 namespace moe {
@@ -146,9 +150,12 @@ __device__ __forceinline__ void norm_out(const NormArgs &a, size_t base, int c, 
     if (a.y && in) store8(Bf16{}, a.y, base + 8 * c, y);
 }
 
-// One block per token, the row in registers.  The square sum and the 8-bit
-// output's values are in 64 bits: the sum cannot overflow whatever the type
-// holds, and a code is the one the exact value rounds to.
+// One block per token, the row in registers, all its loads ahead of the first
+// use: 8192 blocks of 256 threads at H = 4096 keep the memory busy by their
+// number.  (A wave per row for short rows, with no barrier, was no faster: 12.5
+// against 12.0 us for 8192 rows of 1024.)  The square sum and the 8-bit output's
+// values are in 64 bits: the sum cannot overflow whatever the type holds, and a
+// code is the one the exact value rounds to.
 template <typename X, typename R>
 __global__ __launch_bounds__(kWave *kNormMaxWaves) void rms_norm(NormArgs a) {
     __shared__ double part[kNormMaxWaves];
@@ -302,7 +309,9 @@ __device__ __forceinline__ void bwd_terms(const Raw8<DY> &ry, const Raw8<S> &rs,
 
 // At most MW waves per row.  Rows of up to 4096 elements (MW = 4) have the
 // registers for two rows: the block's next token is loaded while the current
-// one is worked on.
+// one is worked on.  8192 x 4096 in bf16: 44 us for 268 MB on inputs that stay
+// the same between calls (column_sum behind it 4 us); 777 x 2176 from a
+// checkpoint 7.9 us and 2 us.
 template <int MW, typename DY, typename S, typename DR, typename DX>
 __global__ __launch_bounds__(kWave *MW) void rms_norm_backward(NormBwdArgs a, float *__restrict__ dwpart) {
     __shared__ float part[2][MW];
@@ -472,7 +481,8 @@ __global__ __launch_bounds__(256) void norm_dweight_wide(NormBwdArgs a, float *_
 }
 
 // Column sums: block = 16 columns, 64 chains of rows (r, r + 64, ...; a wave has
-// four of them side by side), eight rows of a chain in flight.
+// four of them side by side), eight rows of a chain in flight.  512 rows of 4096
+// (8.4 MB, from the caches): 4 us, about 2 of them the launch.
 __global__ __launch_bounds__(1024) void column_sum(const float *__restrict__ part, int R, int C,
                                                    float *__restrict__ out) {
     __shared__ float lds[16][16];
