@@ -458,6 +458,21 @@ def test_route_backward(T, H, E, k, src, renorm, dxt):
     c.check()
 
 
+@pytest.mark.parametrize("src,dxt", [("x", B16), ("q_norm", F32)])
+@pytest.mark.parametrize("T,H,E,k", [(2100, 4224, 40, 3), (2100, 4224, 257, 8), (400, 2176, 65, 2)])
+def test_route_backward_many_tiles(T, H, E, k, src, dxt):
+    """More dx tiles than compute units and hidden tiles that do not divide by
+    the eight XCDs (17 in groups of three, 9 in groups of two)."""
+    c = Route(T, H, E, k, src, True, mask=True, dxt=dxt, seed=E)
+    c.run()
+    c.check()
+    got = c.dx.clone()
+    c.dx.fill_(7.0)
+    c.run(dwr=False)
+    torch.cuda.synchronize()
+    assert torch.equal(c.dx, got)
+
+
 @pytest.mark.parametrize("T", [1500, 2081])
 def test_route_backward_split_tokens(T):
     """Enough tokens that dw_router is summed in parts."""
