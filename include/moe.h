@@ -340,7 +340,8 @@ moe_status moe_fingerprint(const moe_shape *s, const moe_residency *r, const int
  * ------------------------------------------------------------------------- */
 
 /* Bytes of workspace for the entries below, for T tokens in n_seq sequences
- * (0 if an argument is invalid; n_seq in [1, MOE_MAX_SEQS]). */
+ * (0 if an argument is invalid; n_seq in [1, MOE_MAX_SEQS]).  Does not fall as
+ * T or n_seq rise: a workspace for the largest serves every call below it. */
 #define MOE_MAX_SEQS 32768
 size_t moe_train_workspace_bytes(const moe_shape *s, int32_t n_tokens, int32_t n_seq);
 

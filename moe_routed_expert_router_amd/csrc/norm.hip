@@ -276,10 +276,12 @@ namespace {
 // Blocks (partial rows of dweight): about 2048 waves, 512 blocks at least, each
 // with the same number of tokens but the last.  By the sizes alone, so that
 // the order of the sums depends on nothing else.
-int norm_bwd_blocks(int T, int H) {
+int norm_bwd_most(int H) {
     const int waves = row_waves(H);
-    const int most = waves < 4 ? 2048 / waves : 512;
-    const int per = (T + most - 1) / most;
+    return waves < 4 ? 2048 / waves : 512;
+}
+int norm_bwd_blocks(int T, int H) {
+    const int most = norm_bwd_most(H), per = (T + most - 1) / most;
     return per > 0 ? (T + per - 1) / per : 0;
 }
 
@@ -556,7 +558,12 @@ hipError_t launch_column_sum(const char *name, const float *part, int R, int C, 
     return hipGetLastError();
 }
 
-size_t norm_bwd_ws_bytes(int T, int H) { return WsLayout::up((size_t)norm_bwd_blocks(T, H) * H * 4); }
+// Not by norm_bwd_blocks, which falls where a block's token count rises: a
+// workspace for T tokens serves fewer.
+size_t norm_bwd_ws_bytes(int T, int H) {
+    const int most = norm_bwd_most(H);
+    return WsLayout::up((size_t)(T < most ? T : most) * H * 4);
+}
 
 hipError_t launch_rms_norm_backward(const NormBwdArgs &a, char *ws, hipStream_t st) {
     float *part = reinterpret_cast<float *>(ws);

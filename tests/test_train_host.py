@@ -6,6 +6,8 @@ import pytest
 
 moe = pytest.importorskip("moe_routed_expert_router_amd",
                           reason="libmoe.so not built (python moe_routed_expert_router_amd/build.py)")
+
+
 def test_train_workspace_bytes():
     s = moe.shape(4096, 2048, 384, 6)
     w1, w8192 = moe.moe_train_workspace_bytes(s, 1, 1), moe.moe_train_workspace_bytes(s, 8192, 1)
@@ -14,6 +16,17 @@ def test_train_workspace_bytes():
     assert moe.moe_train_workspace_bytes(s, 8192, 32768) >= w8192
     for bad in ((s, -1, 1), (s, 1, 0), (s, 1, 32769), (moe.shape(100, 128, 8, 2), 1, 1)):
         assert moe.moe_train_workspace_bytes(*bad) == 0
+
+
+@pytest.mark.parametrize("H", [128, 1024, 1152, 4096, 16512, 65536])
+@pytest.mark.parametrize("E", [1, 8, 257, 1024])
+def test_train_workspace_serves_fewer_tokens(H, E):
+    s = moe.shape(H, 128, E, 1)
+    near = {m + d for m in (32, 96, 128, 512, 1024, 2048, 4096, 32768, 65536, 1 << 20) for d in (-1, 0, 1)}
+    ts = sorted(t for t in near | set(range(0, 3000, 37)) | {8192, 12345, 100000, 777777} if t <= 1 << 20)
+    for n_seq in (1, 64, 32768):
+        w = [moe.moe_train_workspace_bytes(s, t, n_seq) for t in ts]
+        assert w == sorted(w)
 
 
 def test_train_entries_reject_before_any_launch():
