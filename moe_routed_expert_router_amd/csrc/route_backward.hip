@@ -44,7 +44,6 @@ constexpr int kDzTok = 32;    // tokens per block of route_dz
 struct RouteWs {
     int tg, ec, eg, hg;   // groups: 32 tokens, 16 experts (a multiple of 4), 32 experts, 32 hidden columns
     size_t tscale, hscale, dza, dzt, wrp, valid, dbp, dwp, total;
-    int splits;
 };
 
 constexpr int kTileE = 128, kTileH = 256, kTileT = 128;
@@ -52,15 +51,45 @@ constexpr int kStepK = 32;
 constexpr int kMaxSplits = 16;
 constexpr int kCus = 256;   // compute units: one block of the product kernels on each
 
-// Token splits of the dWr product: as many as keep its (expert, hidden) tiles
-// within one round of blocks, each with at least 4 steps of 32 tokens, at most
-// kMaxSplits (every split writes and re-reads a partial dWr).
-int dw_splits(int T, int H, int E) {
-    const int tiles = ((E + kTileE - 1) / kTileE) * ((H + kTileH - 1) / kTileH);
-    int s = kCus / tiles;
-    const int most = (T + 4 * kStepK - 1) / (4 * kStepK);
+int tiles_of(int n, int tile) { return (n + tile - 1) / tile; }
+
+// The most token splits of the dWr product: as many as keep its (expert,
+// hidden) tiles within one round of blocks, each with at least 4 steps of 32
+// tokens, at most kMaxSplits (every split writes and re-reads a partial dWr).
+int most_splits(int T, int H, int E) {
+    int s = kCus / (tiles_of(E, kTileE) * tiles_of(H, kTileH));
+    const int most = tiles_of(T, 4 * kStepK);
     s = s < most ? s : most;
     return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
+}
+
+// The splits that a call makes.  The most are best for dWr alone, but with dx
+// beside it in the launch fewer leave compute units to dx from the start, whose
+// loads and stores then run beside dWr's MFMAs, and cost fewer ramps and partial
+// sums.  The number with the least estimated time for bf16 dx, whatever the call
+// wants (dWr's bits depend on the sizes alone): the launch takes the longest
+// block, or all of them spread over the compute units.  In tenths of a us,
+// fitted at H 4096, E 384: a block of dWr 100 + 11 per step of 32 tokens, a tile
+// of dx 10 + 9 per step of 64 experts, the sum of a partial 384 x 4096 dWr 12.
+// Whole calls with 5 / 4 / 3 splits, us: 8192 tokens, bf16 dx 115 / 112 / 114
+// (estimate's choice: 4), fp32 dx 165 / 167 / 162, dWr alone 86 / 87 / 96; 2051
+// tokens, bf16 dx 62 / 52 / 50 (choice: 4), fp32 67 / 62 / 65, alone 43 / 44 / 46.
+int dw_splits(int T, int H, int E) {
+    const int most = most_splits(T, H, E);
+    const int tiles = tiles_of(E, kTileE) * tiles_of(H, kTileH), steps = tiles_of(T, kStepK);
+    const int64_t dx_work = (int64_t)tiles_of(T, kTileT) * tiles_of(H, kTileH) * (10 + 9 * tiles_of(E, 64));
+    int best = most;
+    int64_t least = INT64_MAX;
+    for (int s = most; s >= 1; --s) {
+        const int64_t block = 100 + 11 * tiles_of(steps, s), all = (tiles * s * block + dx_work) / kCus;
+        const int64_t longest = tiles_of(tiles * s, kCus) * block;
+        const int64_t time = (all > longest ? all : longest) + (int64_t)s * E * H / 131072;
+        if (time < least) {
+            least = time;
+            best = s;
+        }
+    }
+    return best;
 }
 
 RouteWs route_ws(int T, int H, int E, int terms) {
@@ -69,7 +98,6 @@ RouteWs route_ws(int T, int H, int E, int terms) {
     w.eg = (E + 31) / 32;
     w.ec = 4 * ((E + 63) / 64);
     w.hg = H / 32;
-    w.splits = dw_splits(T, H, E);
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t r = at;
@@ -83,7 +111,7 @@ RouteWs route_ws(int T, int H, int E, int terms) {
     w.wrp = take((size_t)w.hg * w.ec * terms * kUnit);
     w.valid = take((size_t)w.tg * 4);
     w.dbp = take((size_t)w.tg * E * 4);
-    w.dwp = take((size_t)w.splits * E * H * 4);
+    w.dwp = take((size_t)most_splits(T, H, E) * E * H * 4);
     w.total = at;
     return w;
 }
@@ -1160,20 +1188,22 @@ void launch_operands(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStrea
 }
 
 template <int NP, typename DX, bool MX>
-void launch_products(const RouteBwdArgs &a, const RouteWs &w, char *ws, hipStream_t st) {
+void launch_products(const RouteBwdArgs &a, const RouteWs &w, int splits, char *ws, hipStream_t st) {
     const uint8_t *u = reinterpret_cast<const uint8_t *>(ws);
-    const int HT = (a.H + kTileH - 1) / kTileH;
-    const DxTiles t(HT, (a.T + kTileT - 1) / kTileT, (HT + 7) / 8);
-    const int per = (HT * t.TT + 7) / 8;
-    const int n_dx = a.dx ? 8 * (per < kCus / 8 ? per : kCus / 8) : 0;
-    const int tiles = ((a.E + kTileE - 1) / kTileE) * HT * w.splits;
-    const int n_dwr = a.dwr ? 8 * ((tiles + 7) / 8) : 0;
-    float *dwr = w.splits > 1 ? reinterpret_cast<float *>(ws + w.dwp) : a.dwr;
+    const int HT = tiles_of(a.H, kTileH);
+    const DxTiles t(HT, tiles_of(a.T, kTileT), tiles_of(HT, 8));
+    // blocks of dx on an XCD: one per compute unit, or two in turn beside dWr, so
+    // that its units end together (8192 tokens: 112 against 119 us; alone 42.9
+    // against 41.7, as every block has a ramp)
+    const int slots = kCus / 8 * (a.dwr ? 2 : 1), per = tiles_of(HT * t.TT, 8);
+    const int n_dx = a.dx ? 8 * (per < slots ? per : slots) : 0;
+    const int n_dwr = a.dwr ? 8 * tiles_of(tiles_of(a.E, kTileE) * HT * splits, 8) : 0;
+    float *dwr = splits > 1 ? reinterpret_cast<float *>(ws + w.dwp) : a.dwr;
     if (n_dx + n_dwr > 0)
         MOE_LAUNCH("route_products", (route_products<NP, DX, MX>), dim3(n_dwr + n_dx), dim3(512), 0, st, a, u + w.dza,
                    u + w.dzt, u + w.wrp, reinterpret_cast<const int32_t *>(ws + w.tscale),
                    reinterpret_cast<const int32_t *>(ws + w.hscale), reinterpret_cast<const uint32_t *>(ws + w.valid),
-                   w.tg, w.ec, w.eg, w.splits, dwr, n_dwr, t, n_dx);
+                   w.tg, w.ec, w.eg, splits, dwr, n_dwr, t, n_dx);
 }
 
 }  // namespace
@@ -1186,6 +1216,7 @@ size_t route_bwd_ws_bytes(int T, int H, int E) {
 hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st) {
     const int terms = a.dx_dtype == MOE_OUT_F32 ? 2 : 1;   // of dx's factors
     const RouteWs w = route_ws(a.T, a.H, a.E, terms);
+    const int splits = dw_splits(a.T, a.H, a.E);
     const size_t ne = (size_t)a.E * a.H;
     if (a.T == 0) {
         if (a.dwr) MOE_LAUNCH("route_zero", route_zero, dim3(512), dim3(256), 0, st, a.dwr, ne);
@@ -1199,19 +1230,19 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, char *ws, hipStream_t st
         launch_operands<1>(a, w, ws, st);
     const bool mx = a.x == nullptr;
     if (terms == 2 && mx)
-        launch_products<2, float, true>(a, w, ws, st);
+        launch_products<2, float, true>(a, w, splits, ws, st);
     else if (terms == 2)
-        launch_products<2, float, false>(a, w, ws, st);
+        launch_products<2, float, false>(a, w, splits, ws, st);
     else if (mx)
-        launch_products<1, Bf16, true>(a, w, ws, st);
+        launch_products<1, Bf16, true>(a, w, splits, ws, st);
     else
-        launch_products<1, Bf16, false>(a, w, ws, st);
+        launch_products<1, Bf16, false>(a, w, splits, ws, st);
     float *part = reinterpret_cast<float *>(ws + w.dwp);
     const size_t n4 = ne / 4;
-    const int n_dwr = a.dwr && w.splits > 1 ? (int)((n4 + 255) / 256) : 0, n_db = a.db ? (a.E + 63) / 64 : 0;
+    const int n_dwr = a.dwr && splits > 1 ? (int)((n4 + 255) / 256) : 0, n_db = a.db ? (a.E + 63) / 64 : 0;
     if (n_dwr + n_db > 0)
         MOE_LAUNCH("route_sums", route_sums, dim3(n_dwr + n_db), dim3(256), 0, st,
-                   reinterpret_cast<const float4 *>(part), w.splits, n4, a.H / 4,
+                   reinterpret_cast<const float4 *>(part), splits, n4, a.H / 4,
                    reinterpret_cast<const float4 *>(a.q_weight), reinterpret_cast<float4 *>(a.dwr), n_dwr,
                    reinterpret_cast<const float *>(ws + w.dbp), w.tg, a.E, a.db);
     return hipGetLastError();
