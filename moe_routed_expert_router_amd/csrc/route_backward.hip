@@ -890,11 +890,11 @@ __device__ __forceinline__ void dwr_block(const RouteBwdArgs &a, const uint8_t *
     }
 }
 
-// Both products in one launch (8192 tokens, H 4096, E 384, bf16 dx: 102 us where
-// two launches took 39 + 74; 103 GFLOP of issued products, the matrix pipes busy 61%
-// of the cycles, no LDS bank conflicts; dWr's MFMAs alone are 80,000 of its
-// 105,000 cycles at a clock that power holds near 1.8 GHz), a block per compute
-// unit at a time: blocks [0,
+// Both products in one launch (8192 tokens, H 4096, E 384, bf16 dx: 101 us where
+// two launches took 39 + 74; 103 GFLOP of issued products, the matrix pipes busy 62%
+// of the cycles, no LDS bank conflicts; dWr's MFMAs are 80,000 of the 105,000 cycles
+// of 52 steps, at a clock that power holds near 1.8 GHz: with a dz that is mostly
+// zeros the same launch takes 88 us), a block per compute unit at a time: blocks [0,
 // n_dwr) have dWr, the following n_dx dx (both multiples of 8, so that a
 // block's number modulo 8 is its XCD).  The blocks of dx start as those of dWr
 // end: neither waits for the other's last round.
@@ -920,8 +920,8 @@ __global__ __launch_bounds__(512) void route_products(RouteBwdArgs a, const uint
                          rows_ts);
 }
 
-// The sums over blocks (five splits of a 384 x 4096 dWr, 31 MB read and 6 MB
-// written: 7 us).  Blocks [0, n_dwr): dWr from the splits' partials, in
+// The sums over blocks (four splits of a 384 x 4096 dWr, 25 MB read and 6 MB
+// written: 6 us).  Blocks [0, n_dwr): dWr from the splits' partials, in
 // split order, times the checkpoint's column weight; the others: 64 columns of
 // db each from the token groups' parts, four interleaved chains.
 __global__ __launch_bounds__(256) void route_sums(const float4 *__restrict__ part, int splits, size_t n4, int H4,
