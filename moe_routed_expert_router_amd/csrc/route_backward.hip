@@ -178,22 +178,27 @@ __device__ __forceinline__ int scale_exponent(float max) {
 }
 
 // --------------------------------- dz --------------------------------------
-// dz of token t's row: v[i] for expert lane + 64 i (0 past E, for a masked
-// token and for t >= T).
+// dz of token t's row, by one wave, into row[0 .. 64 NPL - 1] of LDS (0 past E, for
+// a masked token and for t >= T).  The picks' parts are added in LDS, each lane
+// its own: in registers every lane would compare its NPL experts with every
+// pick (384 experts, k = 6: the operands of 8192 tokens 12.6 against 13.8 us, of
+// 2048 8.3 against 9.8).
 template <int NPL>
-__device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[NPL]) {
+__device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float *row) {
     const int lane = threadIdx.x & 63, E = a.E, k = a.k;
+    float v[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) v[i] = 0.f;
-    if (t >= a.T || (a.mask && a.mask[t] == 0)) return;
+    const bool in = t < a.T && !(a.mask && a.mask[t] == 0), picks = in && a.dw;
     const size_t at = (size_t)t * E;
-    if (a.dz_in) {
+    if (in && a.dz_in) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
             if (lane + 64 * i < E) v[i] = a.dz_in[at + lane + 64 * i];
     }
-    if (a.dw) {
-        int id = -1;
+    int id = -1;
+    float part = 0.f;   // of lane j: what pick j adds to its expert
+    if (picks) {
         float w = 0.f, d = 0.f;
         if (lane < k) {
             id = a.ids[(size_t)t * k + lane];
@@ -204,14 +209,7 @@ __device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[
         // a pick outside [0, E) added nothing to the output: its weight has no gradient
         const float dot = wave_sum(id >= 0 ? w * d : 0.f);
         if (a.renorm) {
-            const float u = w * ((id >= 0 ? d : 0.f) - dot);
-            for (int j = 0; j < k; ++j) {
-                const int ej = __builtin_amdgcn_readlane(id, j);
-                const float uj = readlanef(u, j);
-#pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (lane + 64 * i == ej) v[i] += uj;
-            }
+            part = w * (d - dot);
         } else {
             float z[NPL], m = -INFINITY, s = 0.f;
 #pragma unroll
@@ -223,26 +221,31 @@ __device__ __forceinline__ void dz_row(const RouteBwdArgs &a, int t, float (&v)[
             }
             m = wave_max(m);
             m = m == -INFINITY ? 0.f : m;
-            float g[NPL];
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
                 z[i] = expf(z[i] - m);
                 s += z[i];
-                g[i] = -dot;
             }
             s = wave_sum(s);
             const float inv = s == 0.f ? 0.f : 1.f / s;
-            for (int j = 0; j < k; ++j) {
-                const int ej = __builtin_amdgcn_readlane(id, j);
-                const float dj = readlanef(d, j);
 #pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (lane + 64 * i == ej) g[i] += dj;
+            for (int i = 0; i < NPL; ++i) {
+                z[i] *= inv;
+                row[lane + 64 * i] = z[i];
+                v[i] = fmaf(z[i], -dot, v[i]);
             }
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) v[i] = fmaf(z[i] * inv, g[i], v[i]);
+            if (id >= 0) part = row[id] * d;
         }
     }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) row[lane + 64 * i] = v[i];
+    if (!picks) return;
+    // each expert's first pick at once, repeated ones behind them in order
+    bool again = false;
+    for (int j = 0; j + 1 < k; ++j) again |= lane > j && id == __builtin_amdgcn_readlane(id, j);
+    if (id >= 0 && !again) row[id] += part;
+    for (uint64_t left = __ballot(id >= 0 && again); left != 0; left &= left - 1)
+        if (lane == __builtin_ctzll(left)) row[id] += part;
 }
 
 // 32 columns of Wr [E][H] as scaled units (32 hidden columns, 16 experts), the
@@ -292,8 +295,8 @@ __device__ void wr_units(const RouteBwdArgs &a, uint8_t *__restrict__ out, int32
 }
 
 // The operands of both products, so that the dz and Wr values are split once
-// and not by every block that uses them.  8192 tokens, H 4096, E 384: 13.3 us
-// for 25 MB read and 29 MB written (4 TB/s).  Blocks [0, tg): 32 tokens each, a wave per
+// and not by every block that uses them.  8192 tokens, H 4096, E 384: 12.6 us
+// for 25 MB read and 29 MB written (4.3 TB/s).  Blocks [0, tg): 32 tokens each, a wave per
 // token at a time: dz of the row in registers, then in an LDS tile from which
 // it leaves in both operand orders (token rows for dx, expert rows for dWr)
 // and as the block's part of db; tokens past T and masked tokens have dz = 0.
@@ -314,24 +317,20 @@ __global__ __launch_bounds__(1024) void route_operands(RouteBwdArgs a, uint8_t *
         return;
     }
     float(*tile)[kPitch] = reinterpret_cast<float(*)[kPitch]>(lds);
-    {
-        float v[2][NPL];
-        dz_row<NPL>(a, tok0 + wave, v[0]);
-        dz_row<NPL>(a, tok0 + wave + 16, v[1]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+    for (int q = 0; q < 2; ++q) dz_row<NPL>(a, tok0 + wave + 16 * q, tile[wave + 16 * q]);
+    if (dza) {   // after both rows, whose loads are then not behind a row's maximum
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = wave + 16 * q;
             float m = 0.f;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                tile[wave + 16 * r][lane + 64 * i] = v[r][i];
-                const float u = fabsf(v[r][i]);
+                const float u = fabsf(tile[r][lane + 64 * i]);
                 m = u < INFINITY ? fmaxf(m, u) : INFINITY;
             }
             const int sc = scale_exponent(wave_max(m));
-            if (lane == 0) {
-                tsc[wave + 16 * r] = sc;
-                if (dza) tscale[tok0 + wave + 16 * r] = sc;
-            }
+            if (lane == 0) tscale[tok0 + r] = tsc[r] = sc;
         }
     }
     if (wave == 0) {   // a bit per token of the group that counts
@@ -980,13 +979,14 @@ constexpr int kFewTokens = 96;
 
 template <int NPL>
 __global__ __launch_bounds__(256) void route_dz_rows(RouteBwdArgs a, float *__restrict__ dz, int E8) {
+    __shared__ float rows[4][64 * NPL];
     const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (t >= a.T) return;
-    float v[NPL];
-    dz_row<NPL>(a, t, v);
+    float *const row = rows[threadIdx.x >> 6];
+    dz_row<NPL>(a, t, row);
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-        if (lane + 64 * i < E8) dz[(size_t)t * E8 + lane + 64 * i] = v[i];
+        if (lane + 64 * i < E8) dz[(size_t)t * E8 + lane + 64 * i] = row[lane + 64 * i];
 }
 
 // D += A B, lane l: A[l % 32][l / 32], B[l / 32][l % 32]; D as in mfma32x32x16.
