@@ -889,7 +889,7 @@ __device__ __forceinline__ void dwr_block(const RouteBwdArgs &a, const uint8_t *
     }
 }
 
-// Both products in one launch (8192 tokens, H 4096, E 384, bf16 dx: 101 us where
+// Both products in one launch (8192 tokens, H 4096, E 384, bf16 dx: 100 us where
 // two launches took 39 + 74; 103 GFLOP of issued products, the matrix pipes busy 62%
 // of the cycles, no LDS bank conflicts; dWr's MFMAs are 80,000 of the 105,000 cycles
 // of 52 steps, at a clock that power holds near 1.8 GHz: with a dz that is mostly
