@@ -327,6 +327,37 @@ def test_balance_nonfinite_rows(T):
     assert r["loss"].item() == 0 and torch.all(r["dlogits"] == 0) and r["n_valid"].tolist() == [T, 1]
 
 
+@pytest.mark.parametrize("E", [40, 257, 1024])
+@pytest.mark.parametrize("T", [300, 1000])
+def test_balance_one_group_in_parts(T, E):
+    """One group added up by several blocks: non-finite parts from any of
+    them, the largest sum there is (every pick the same expert, probability
+    1), and the same workspace call after call."""
+    k = 32
+    s = moe.shape(128, 128, E, k)
+    z, ids = routing(9, T, E, k)
+    ws = new_ws(s, T)
+    ws.fill_(0xFF)
+    good = balance(s, z, ids, None, None, 0.1, ws=ws)
+    check_balance(good, z, ids, None, None, 0.1, k)
+    for bad in (float("nan"), float("inf")):
+        for e in (0, E - 1):
+            y = z.clone()
+            y[T - 2, e] = bad
+            r = balance(s, y, ids, None, None, 0.1, ws=ws)
+            torch.cuda.synchronize()
+            assert torch.isnan(r["loss"]).all() and r["n_valid"].tolist() == [T, 1]
+            assert torch.equal(r["counts"], good["counts"])
+    y = torch.zeros((T, E), device="cuda")
+    y[:, E - 1] = 200.0   # the others' exp is 0
+    r = balance(s, y, torch.full_like(ids, E - 1), None, None, 0.25, ws=ws)
+    torch.cuda.synchronize()
+    assert r["loss"].item() == 0.25 * E and r["counts"][0, E - 1].item() == T * k
+    again = balance(s, z, ids, None, None, 0.1, ws=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(good[n], again[n]) for n in good)
+
+
 def test_balance_in_place():
     s = moe.shape(128, 128, 40, 3)
     z, ids = routing(2, 300, 40, 3)
